@@ -16,3 +16,7 @@ from .ops import (  # noqa: E402,F401
     weight_kurtosis, moe_lowrank_prepass, moe_w3a16_lowrank_gemm, pack_int3,
     pack_lr_int3, packed_words, quantize_hqq_int3, quantize_rtn_int3, route_sort, sz_words,
 )
+from .moe16 import (  # noqa: E402,F401
+    MoELayer16, moe_linear, moe_linear_act_grad, moe_linear_grad, moe_permute, moe_permute_grad, moe_unpermute,
+    moe_unpermute_grad, route_grad,
+)

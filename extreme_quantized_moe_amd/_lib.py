@@ -14,6 +14,8 @@ GEMM_PREPASS_DONE = 1
 STATIC_WORKSPACE_BYTES = 64 << 20
 LR_FP16, LR_INT3 = 0, 1
 QUANT_RTN, QUANT_HQQ = 0, 1
+F16, BF16, F32 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 
 
 class MiloWeights(C.Structure):
@@ -33,6 +35,25 @@ class MiloGemmDesc(C.Structure):
         ("num_pairs", C.c_int32), ("max_rows_per_expert", C.c_int32),
         ("slot_w", C.c_void_p), ("y_rows", C.c_int32), ("epilogue", C.c_int32),
         ("y", C.c_void_p), ("path", C.c_int32), ("flags", C.c_int32),
+    ]
+
+
+class MiloLinearDesc(C.Structure):
+    _fields_ = [
+        ("num_experts", C.c_int32), ("N", C.c_int32), ("K", C.c_int32), ("num_rows", C.c_int32),
+        ("max_rows_per_expert", C.c_int32), ("dtype", C.c_int32), ("out_dtype", C.c_int32),
+        ("activation", C.c_int32),
+        ("x", C.c_void_p), ("w", C.c_void_p), ("offsets", C.c_void_p), ("bias", C.c_void_p),
+        ("mul", C.c_void_p), ("residual", C.c_void_p), ("pre", C.c_void_p), ("y", C.c_void_p),
+    ]
+
+
+class MiloLinearGradDesc(C.Structure):
+    _fields_ = [
+        ("num_experts", C.c_int32), ("N", C.c_int32), ("K", C.c_int32), ("num_rows", C.c_int32),
+        ("dtype", C.c_int32), ("dw_dtype", C.c_int32),
+        ("dy", C.c_void_p), ("x", C.c_void_p), ("w", C.c_void_p), ("offsets", C.c_void_p),
+        ("dx_add", C.c_void_p), ("dx", C.c_void_p), ("dw", C.c_void_p),
     ]
 
 
@@ -89,6 +110,17 @@ def lib():
         "milo_moe_lowrank_prepass": (i32, [C.POINTER(MiloGemmDesc), vp, sz, vp]),
         "milo_moe_w3a16_lowrank_gemm_static": (i32, [C.POINTER(MiloGemmDesc), vp]),
         "milo_moe_combine": (i32, [vp, i32, i32, i32, vp, vp]),
+        "milo_moe_permute": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "milo_moe_permute_grad": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "milo_moe_unpermute": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "milo_moe_unpermute_grad": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+        "milo_route_grad": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "milo_moe_linear_workspace_bytes": (sz, [C.POINTER(MiloLinearDesc)]),
+        "milo_moe_linear": (i32, [C.POINTER(MiloLinearDesc), vp, sz, vp]),
+        "milo_moe_linear_act_grad_workspace_bytes": (sz, [i32, i32, i32]),
+        "milo_moe_linear_act_grad": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]),
+        "milo_moe_linear_grad_workspace_bytes": (sz, [C.POINTER(MiloLinearGradDesc)]),
+        "milo_moe_linear_grad": (i32, [C.POINTER(MiloLinearGradDesc), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

@@ -1,0 +1,54 @@
+// The storage types of the 16-bit (and 32-bit) MoE operators: conversion to
+// float, rounding back (nearest even), and one 8-wide matrix-core operand.
+#pragma once
+
+#include "milo_internal.hpp"
+
+namespace milo {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+struct F16 {
+  typedef uint16_t store;
+  static __device__ __forceinline__ float up(uint16_t b) { return half_bits_to_float(b); }
+  static __device__ __forceinline__ uint16_t down(float v) { return float_to_half_bits(v); }
+  static __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                  0, 0);
+  }
+};
+
+struct BF16 {
+  typedef uint16_t store;
+  static __device__ __forceinline__ float up(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+  static __device__ __forceinline__ uint16_t down(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+  static __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+  }
+};
+
+struct F32 {
+  typedef float store;
+  static __device__ __forceinline__ float up(float v) { return v; }
+  static __device__ __forceinline__ float down(float v) { return v; }
+};
+
+// V consecutive elements, loaded and stored as one access (V sizeof(store)
+// bytes, aligned to that).
+template <class T, int V>
+struct alignas(V * sizeof(typename T::store)) Pack {
+  typename T::store v[V];
+};
+
+// Largest access width in bytes, at most 16, that row lengths of `row_bytes`
+// and all the given addresses allow.
+inline int access_bytes(size_t row_bytes, const void* a, const void* b = nullptr, const void* c = nullptr,
+                        const void* d = nullptr) {
+  const uintptr_t bits = (uintptr_t)row_bytes | (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)d;
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+
+}  // namespace milo

@@ -1,0 +1,236 @@
+// What the 16-bit grouped product kernels share: arguments, the rows of an
+// expert, the tile order, the activations and the epilogue.
+//
+//   forward  C[p][n]    = sum_k x[p][k] w[e][n][k],   p of expert e; epilogue
+//   dx       C[p][k]    = sum_n dy[p][n] w[e][n][k]
+//   dw       C[e][n][k] = sum_p dy[p][n] x[p][k],     p over expert e's rows
+//
+// Each is C[m][n] = sum_c A[m][c] B[n][c].  An operand is "deep" where the
+// contraction index c is the contiguous one in memory and "wide" where m (or
+// n) is: forward deep x deep, dx deep x wide, dw wide x wide.
+#pragma once
+
+#include "half_types.hpp"
+
+namespace milo {
+
+enum { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct LinearArgs {
+  const void* a;            // fwd: x; dx, dw: dy
+  const void* b;            // fwd, dx: w; dw: x
+  const int32_t* offsets;   // NULL: one expert owns every row
+  const void* bias;         // each may be NULL; bias, mul, pre: forward only
+  const void* mul;
+  const void* residual;     // dx: the other gradient added
+  void* pre;
+  void* out;
+  float* part;              // split contraction: partial sums
+  int E, rows, N, K;
+  int max_rows;             // host bound on an expert's rows (plan only)
+  int act;
+  int out_f32;              // out holds float32 instead of the 16-bit type
+  int splits;               // parts of the contraction (1: not split)
+};
+
+// Expert e's rows [base, base + rows); the table is clipped to the buffer, so
+// no table makes a kernel read or write outside it.
+struct Span {
+  int base, rows;
+};
+
+__device__ __forceinline__ Span clip_span(int lo, int hi, int total) {
+  lo = lo < 0 ? 0 : lo > total ? total : lo;
+  hi = hi < lo ? lo : hi > total ? total : hi;
+  return {lo, hi - lo};
+}
+
+__device__ __forceinline__ Span expert_span(const int32_t* __restrict__ offsets, int e, int total) {
+  if (!offsets) return {0, total};
+  return clip_span(offsets[e], offsets[e + 1], total);
+}
+
+// Row tile `id` of `id = row_tile * width + column` when every expert's rows
+// are cut into tiles of `tile_rows`: wave-uniform, no LDS, no barrier.  Up to
+// 256 experts, four to a lane group.  total: number of ids over all experts.
+struct TileSlot {
+  int e;          // -1: past the last tile
+  Span span;
+  int local;      // id within the expert, 0 .. row_tiles * width - 1
+  int row_tiles;  // of this expert
+  int first;      // row tiles before this expert's
+};
+
+template <class Remap>
+__device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offsets, int E, int total_rows,
+                                              int tile_rows, int width, Remap remap) {
+  TileSlot s;
+  if (!offsets || E == 1) {
+    s.span = expert_span(offsets, 0, total_rows);
+    s.row_tiles = (s.span.rows + tile_rows - 1) / tile_rows;
+    s.first = 0;
+    s.local = remap(s.row_tiles * width);
+    s.e = s.local >= 0 && s.local < s.row_tiles * width ? 0 : -1;
+    return s;
+  }
+  const int lane = threadIdx.x & 63;
+  int lo[4], n[4], incl[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int e = 64 * c + lane, ec = e < E ? e : E - 1;
+    const Span p = clip_span(offsets[ec], offsets[ec + 1], total_rows);
+    lo[c] = p.base;
+    n[c] = e < E ? p.rows : 0;
+  }
+  int before = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    int v = (n[c] + tile_rows - 1) / tile_rows;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(v, d);
+      if (lane >= d) v += u;
+    }
+    incl[c] = before + v;
+    before = __shfl(incl[c], 63);
+  }
+  const int id = remap(before * width);
+  s.e = -1;
+  s.span = {0, 0};
+  s.local = s.row_tiles = s.first = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int tiles = (n[c] + tile_rows - 1) / tile_rows, first = incl[c] - tiles;
+    const uint64_t hit = __ballot(id >= 0 && id >= first * width && id < incl[c] * width);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      s.e = 64 * c + src;
+      s.span.base = __builtin_amdgcn_readlane(lo[c], src);
+      s.span.rows = __builtin_amdgcn_readlane(n[c], src);
+      s.first = __builtin_amdgcn_readlane(first, src);
+      s.row_tiles = __builtin_amdgcn_readlane(tiles, src);
+      s.local = id - s.first * width;
+    }
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------- activations
+// Float32 values; the tails are computed without cancellation (erfc, sigmoid)
+// so that they are right to float32 relative precision, and arguments are
+// bounded where a product of 0 and infinity would appear.  NaN stays NaN.
+__device__ __forceinline__ float bounded(float v, float lo, float hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kTanhC = 0.79788456080286536f;       // sqrt(2 / pi)
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+__device__ __forceinline__ float act_value(int act, float v) {
+  switch (act) {
+    case MILO_ACT_RELU: return v < 0.f ? 0.f : v;
+    case MILO_ACT_SILU: v = v < -1e3f ? -1e3f : v; return v * sigmoid(v);
+    case MILO_ACT_GELU: v = v < -1e3f ? -1e3f : v; return 0.5f * v * erfcf(-v * kSqrtHalf);
+    case MILO_ACT_GELU_TANH:
+      v = v < -1e3f ? -1e3f : v;
+      return v * sigmoid(2.f * kTanhC * __builtin_fmaf(0.044715f * v * v, v, v));
+    default: return v;
+  }
+}
+
+// act(v) and act'(v); relu'(0) = 0.
+__device__ __forceinline__ float act_slope(int act, float v, float* value) {
+  switch (act) {
+    case MILO_ACT_RELU: *value = v < 0.f ? 0.f : v; return v > 0.f ? 1.f : v <= 0.f ? 0.f : v;
+    case MILO_ACT_SILU: {
+      const float b = bounded(v, -1e3f, 1e3f), g = sigmoid(b);
+      *value = (v > b ? v : b) * g;
+      return g * __builtin_fmaf(b, 1.f - g, 1.f);
+    }
+    case MILO_ACT_GELU: {
+      const float b = bounded(v, -1e3f, 1e3f), cdf = 0.5f * erfcf(-b * kSqrtHalf);
+      *value = (v > b ? v : b) * cdf;
+      return __builtin_fmaf(b * kInvSqrt2Pi, expf(-0.5f * b * b), cdf);
+    }
+    case MILO_ACT_GELU_TANH: {
+      const float b = bounded(v, -1e3f, 1e3f);
+      const float g = sigmoid(2.f * kTanhC * __builtin_fmaf(0.044715f * b * b, b, b));
+      *value = (v > b ? v : b) * g;
+      // d/dv of v g(2 u), u' = c (1 + 3 0.044715 v^2)
+      return __builtin_fmaf(b * g * (1.f - g), 2.f * kTanhC * __builtin_fmaf(3.f * 0.044715f * b, b, 1.f), g);
+    }
+    default: *value = v; return 1.f;
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+// V consecutive columns of one row.  V > 1 needs every array's row length and
+// address to allow V-wide accesses (the launcher's rule).  Forward: bias, the
+// kept pre-activation, activation, gate operand, residual, all in float32,
+// one rounding at each store.
+template <class T, int MODE, int V>
+__device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, int col, const float* v_in) {
+  const int ld = MODE == kFwd ? a.N : a.K;
+  const int64_t at = (MODE == kDw ? ((int64_t)e * a.N + row) : row) * ld + col;
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = v_in[i];
+  if constexpr (MODE == kFwd) {
+    typedef Pack<T, V> P;
+    if (a.bias) {
+      const P b = *(const P*)((const uint16_t*)a.bias + (int64_t)e * ld + col);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += T::up(b.v[i]);
+    }
+    if (a.pre) {
+      P p;
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.v[i] = T::down(v[i]);
+      *(P*)((uint16_t*)a.pre + at) = p;
+    }
+    if (a.act != MILO_ACT_NONE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_value(a.act, v[i]);
+    }
+    if (a.mul) {
+      const P m = *(const P*)((const uint16_t*)a.mul + at);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= T::up(m.v[i]);
+    }
+  }
+  if (MODE != kDw && a.residual) {
+    const Pack<T, V> r = *(const Pack<T, V>*)((const uint16_t*)a.residual + at);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] += T::up(r.v[i]);
+  }
+  if (a.out_f32) {
+    Pack<F32, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v[i] = v[i];
+    *(Pack<F32, V>*)((float*)a.out + at) = o;
+  } else {
+    Pack<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v[i] = T::down(v[i]);
+    *(Pack<T, V>*)((uint16_t*)a.out + at) = o;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// How one product is run (host side; chosen from sizes, types and alignment).
+struct LinearPlan {
+  int kernel;          // kPlan*
+  int splits;
+  size_t part_bytes;   // fp32 partial sums of a split contraction
+};
+enum { kPlanNone = 0, kPlanGeneral };
+
+LinearPlan plan_linear(int mode, const LinearArgs& a);
+int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
+size_t act_grad_workspace_bytes(int E, int N, int rows);
+int32_t launch_act_grad(const void* dy, const void* pre, const void* mul, const int32_t* offsets, int E, int N,
+                        int rows, int dtype, int act, void* dpre, void* dmul, float* dbias, float* part,
+                        hipStream_t st);
+
+}  // namespace milo

@@ -234,6 +234,16 @@ int32_t launch_route(const float* logits, int T, int E, int k, int S, int renorm
                      int32_t* pair_pos, int32_t* offsets, void* ws, hipStream_t st);
 int32_t launch_combine(const float* y, int T, int slots, int H, uint16_t* out, hipStream_t st);
 
+// rows to the experts and back (dispatch.hip)
+int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
+                       void* y, hipStream_t st);
+int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int64_t tokens, int slots, int H,
+                         int64_t rows, int dtype, void* out, hipStream_t st);
+int32_t launch_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
+                              int slots, int H, int64_t rows, int dtype, void* dy, float* dw, hipStream_t st);
+int32_t launch_route_grad(const float* dslot_w, const float* logits, const int32_t* ids, int64_t tokens, int E, int k,
+                          int S, int renorm, float* dlogits, hipStream_t st);
+
 // compensator construction (builder.hip)
 size_t svd_workspace_bytes(int64_t N, int64_t K, int l);
 size_t build_workspace_bytes(int64_t N, int64_t K, int l);

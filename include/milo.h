@@ -504,6 +504,175 @@ int32_t milo_moe_w3a16_lowrank_gemm_static(const milo_gemm_desc* desc, void* str
 int32_t milo_moe_combine(const float* y, int32_t T, int32_t slots, int32_t H,
                          uint16_t* out, void* stream);
 
+/* ======================================================================
+ * The 16-bit MoE block: rows to the experts and back, grouped products with
+ * an epilogue, and their gradients ([talk] Background: the layer MiLo
+ * quantizes; MiLo Algorithm: parts of the model stay in 16 bits)
+ * ====================================================================== */
+
+/* Element types of the operators below (bit patterns of IEEE binary16,
+   bfloat16, IEEE binary32). */
+enum { MILO_F16 = 0, MILO_BF16 = 1, MILO_F32 = 2 };
+
+/*
+ * Rows in expert order and back.  A pair (t, j) is slot j of token t;
+ * pair_pos[t*slots + j] is its row in the expert-ordered buffer (the pair_pos
+ * of milo_route_sort), or a negative value for a dropped pair (e.g. past an
+ * expert's capacity).  A value >= num_rows counts as dropped too.  Two pairs
+ * must not name the same row (what such a row holds is then undefined).
+ *   permute         y[pair_pos[t,j]] = x[t]
+ *   permute_grad    dx[t] = sum over kept j of dy[pair_pos[t,j]]
+ *   unpermute       out[t] = sum over kept j of slot_w[t,j] * y[pair_pos[t,j]]
+ *   unpermute_grad  dy[pair_pos[t,j]] = slot_w[t,j] * dout[t];
+ *                   dslot_w[t,j] = <dout[t], y[pair_pos[t,j]]> (0 if dropped)
+ * Sums run in float32, in slot order (dslot_w: in a fixed order over the
+ * row), and are rounded once.  A token without a kept pair gets zeros.  Rows
+ * of an expert-ordered output that no pair names are not written.
+ *
+ * x, out, dout, dx : [T][H];  y, dy : [num_rows][H], all of type dtype
+ *   (MILO_F16, MILO_BF16 or MILO_F32).  Outputs must not overlap inputs.
+ * slot_w  : float32 [T*slots], or NULL for weights of 1.
+ * dslot_w : out, float32 [T*slots], or NULL (not computed).
+ * Constraints: 0 <= T <= 2^24, 1 <= slots <= 16, 1 <= H <= 2^20,
+ * 0 <= num_rows <= 2^28; pointers aligned to their element (16 bytes where
+ * H rows of 16-byte multiples are to move at full speed).  T == 0 does nothing.
+ * Pointers of buffers without an element may be NULL.
+ */
+int32_t milo_moe_permute(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
+                         int32_t num_rows, int32_t dtype, void* y, void* stream);
+int32_t milo_moe_permute_grad(const void* dy, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
+                              int32_t num_rows, int32_t dtype, void* dx, void* stream);
+int32_t milo_moe_unpermute(const void* y, const int32_t* pair_pos, const float* slot_w, int32_t T,
+                           int32_t slots, int32_t H, int32_t num_rows, int32_t dtype, void* out,
+                           void* stream);
+int32_t milo_moe_unpermute_grad(const void* dout, const void* y, const int32_t* pair_pos,
+                                const float* slot_w, int32_t T, int32_t slots, int32_t H,
+                                int32_t num_rows, int32_t dtype, void* dy, float* dslot_w, void* stream);
+
+/*
+ * Gradient of milo_route_sort's routed weights with respect to the logits
+ * (the selection itself is constant; shared slots' weights are constants):
+ *   renormalize != 0: w = softmax over the k picks;
+ *       dlogits[t][i] = w_i (g_i - sum_j w_j g_j) for a pick i, 0 elsewhere
+ *   renormalize == 0: w = p at the picks, p = softmax over all E;
+ *       dlogits[t][e] = p_e (g_e [e picked] - sum over picks j of p_j g_j)
+ * with g_j = dslot_w[t*(k+S) + j].
+ * dslot_w : float32 [T*(k+S)] (entries of shared slots are not read).
+ * logits  : float32 [T][E], finite;  topk_ids : int32 [T][k], distinct per token.
+ * dlogits : out, float32 [T][E].
+ * Constraints: 0 <= T <= 2^24, 1 <= k <= min(E, 8), 0 <= S, E + S <= 256, k + S <= 16.
+ */
+int32_t milo_route_grad(const float* dslot_w, const float* logits, const int32_t* topk_ids, int32_t T,
+                        int32_t E, int32_t k, int32_t S, int32_t renormalize, float* dlogits, void* stream);
+
+/*
+ * Grouped 16-bit product with an epilogue.  Rows [offsets[e], offsets[e+1])
+ * of x belong to expert e; for each such row p
+ *     pre[p] = x[p] . w[e]^T + bias[e]
+ *     y[p]   = act(pre[p]) * mul[p] + residual[p]
+ * with float32 accumulation, the epilogue in float32 and one rounding at each
+ * store.  One expert is a plain linear layer; SwiGLU experts are two calls
+ * (up product, then the gate product with MILO_ACT_SILU and mul = up).
+ * act: MILO_ACT_NONE, RELU, SILU v/(1+exp(-v)), GELU v Phi(v) (erf form),
+ * GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))).
+ *
+ * dtype     : type of x, w, bias, mul, residual, pre: MILO_F16 or MILO_BF16.
+ * out_dtype : type of y: dtype, or MILO_F32 (e.g. router logits).
+ * x         : [num_rows][K];  w : [num_experts][N][K].
+ * offsets   : int32 [num_experts + 1], non-decreasing (entries are clipped to
+ *             0..num_rows); NULL with num_experts == 1: every row is its.
+ *             Rows before offsets[0] or behind offsets[num_experts] are
+ *             neither read nor written.
+ * bias      : [num_experts][N] or NULL;  mul, residual : [num_rows][N] or NULL.
+ * pre       : out, [num_rows][N] or NULL (kept for the backward pass).
+ * y         : out, [num_rows][N]; may be mul's or residual's own buffer when
+ *             the types are equal, no other overlap of outputs with inputs.
+ * max_rows_per_expert : host upper bound on an expert's rows (0: num_rows);
+ *             only the choice of kernels depends on it, never a result's
+ *             correctness.
+ * workspace : milo_moe_linear_workspace_bytes(desc) bytes (may be 0), 256-byte
+ *             aligned, scratch only.  Calls that overlap in time need
+ *             workspaces of their own.
+ * Capturable into a HIP graph.  Constraints: 1 <= num_experts <= 256,
+ * 1 <= N, K <= 65536, 0 <= num_rows <= 2^20, all pointers aligned to their element (16 bytes, with N
+ * and K multiples of 8, for the fast kernels).  num_rows == 0 does nothing.
+ */
+enum { MILO_ACT_NONE = 0, MILO_ACT_RELU = 1, MILO_ACT_SILU = 2, MILO_ACT_GELU = 3, MILO_ACT_GELU_TANH = 4 };
+
+typedef struct milo_linear_desc {
+  int32_t num_experts;
+  int32_t N, K;
+  int32_t num_rows;
+  int32_t max_rows_per_expert;
+  int32_t dtype;
+  int32_t out_dtype;
+  int32_t activation;
+  const void* x;
+  const void* w;
+  const int32_t* offsets;
+  const void* bias;
+  const void* mul;
+  const void* residual;
+  void* pre;
+  void* y;
+} milo_linear_desc;
+
+size_t milo_moe_linear_workspace_bytes(const milo_linear_desc* desc);
+int32_t milo_moe_linear(const milo_linear_desc* desc, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient through that epilogue (the residual's gradient is dy itself):
+ *     dpre[p] = dy[p] * mul[p] * act'(pre[p])      (relu'(0) = 0)
+ *     dmul[p] = dy[p] * act(pre[p])
+ *     dbias[e] = sum over expert e's rows of dpre, before its rounding
+ * pre   : the kept pre-activation (num_rows x N, type dtype).
+ * mul   : NULL or as in the forward call; dmul : out, required with mul, else NULL.
+ * dbias : out, float32 [num_experts][N], or NULL.  Experts without rows get 0.
+ * workspace : milo_moe_linear_act_grad_workspace_bytes(...) bytes with dbias
+ *   (0 without), 256-byte aligned.
+ * dpre and dmul may be dy's, pre's or mul's own buffers.  Other rules as milo_moe_linear.
+ */
+size_t milo_moe_linear_act_grad_workspace_bytes(int32_t num_experts, int32_t N, int32_t num_rows);
+int32_t milo_moe_linear_act_grad(const void* dy, const void* pre, const void* mul, const int32_t* offsets,
+                                 int32_t num_experts, int32_t N, int32_t num_rows, int32_t dtype,
+                                 int32_t activation, void* dpre, void* dmul, float* dbias, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of the product itself, dy = dpre of the call above (or the
+ * output's gradient where there is no activation):
+ *     dx[p] = dy[p] . w[e] (+ dx_add[p])        for rows p of expert e
+ *     dw[e] = sum over rows p of e of dy[p]^T x[p]   (0 without rows)
+ * float32 accumulation, one rounding.
+ * dy : [num_rows][N], x : [num_rows][K], w : [num_experts][N][K], type dtype.
+ * dx : out, [num_rows][K], or NULL (w is then not read and may be NULL).
+ * dx_add : [num_rows][K] of type dtype, added in float32 before dx is rounded
+ *      (the gradient of the same x from another product), or NULL; may be
+ *      dx's own buffer.
+ * dw : out, [num_experts][N][K] of dw_dtype (dtype or MILO_F32), or NULL (x
+ *      is then not read and may be NULL).
+ * workspace : milo_moe_linear_grad_workspace_bytes(desc) bytes, 256-byte
+ *   aligned.  Other rules as milo_moe_linear.
+ */
+typedef struct milo_linear_grad_desc {
+  int32_t num_experts;
+  int32_t N, K;
+  int32_t num_rows;
+  int32_t dtype;
+  int32_t dw_dtype;
+  const void* dy;
+  const void* x;
+  const void* w;
+  const int32_t* offsets;
+  const void* dx_add;
+  void* dx;
+  void* dw;
+} milo_linear_grad_desc;
+
+size_t milo_moe_linear_grad_workspace_bytes(const milo_linear_grad_desc* desc);
+int32_t milo_moe_linear_grad(const milo_linear_grad_desc* desc, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif
