@@ -121,7 +121,12 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offset
 // bounded where a product of 0 and infinity would appear.  NaN stays NaN.
 __device__ __forceinline__ float bounded(float v, float lo, float hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
+// From exp(-|v|), which never overflows: far negative tails keep their value
+// down to the smallest float32.
+__device__ __forceinline__ float sigmoid(float v) {
+  const float e = expf(-__builtin_fabsf(v));
+  return (v < 0.f ? e : 1.f) / (1.f + e);
+}
 
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kTanhC = 0.79788456080286536f;       // sqrt(2 / pi)
