@@ -94,7 +94,7 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offset
     incl[c] = before + v;
     before = __shfl(incl[c], 63);
   }
-  const int id = remap(before * width);
+  const int id = remap(__builtin_amdgcn_readfirstlane(before) * width);
   s.e = -1;
   s.span = {0, 0};
   s.local = s.row_tiles = s.first = 0;
@@ -103,8 +103,8 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offset
     const int tiles = (n[c] + tile_rows - 1) / tile_rows, first = incl[c] - tiles;
     const uint64_t hit = __ballot(id >= 0 && id >= first * width && id < incl[c] * width);
     if (hit) {
-      const int src = __builtin_ctzll(hit);
-      s.e = 64 * c + src;
+      const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(hit));
+      s.e = 64 * c + src;     // scalar values, so that what follows from them is scalar too
       s.span.base = __builtin_amdgcn_readlane(lo[c], src);
       s.span.rows = __builtin_amdgcn_readlane(n[c], src);
       s.first = __builtin_amdgcn_readlane(first, src);
@@ -210,10 +210,14 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, 
     for (int i = 0; i < V; ++i) v[i] += T::up(r.v[i]);
   }
   if (a.out_f32) {
-    Pack<F32, V> o;
+    constexpr int W = V < 4 ? V : 4;        // at most 16 bytes an access
 #pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = v[i];
-    *(Pack<F32, V>*)((float*)a.out + at) = o;
+    for (int p = 0; p < V / W; ++p) {
+      Pack<F32, W> o;
+#pragma unroll
+      for (int i = 0; i < W; ++i) o.v[i] = v[p * W + i];
+      *(Pack<F32, W>*)((float*)a.out + at + p * W) = o;
+    }
   } else {
     Pack<T, V> o;
 #pragma unroll
@@ -229,10 +233,12 @@ struct LinearPlan {
   int splits;
   size_t part_bytes;   // fp32 partial sums of a split contraction
 };
-enum { kPlanNone = 0, kPlanGeneral };
+enum { kPlanGeneral = 0, kPlanTile128, kPlanTile256 };
 
 LinearPlan plan_linear(int mode, const LinearArgs& a);
 int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
+int32_t launch_linear_general(int mode, int dtype, const LinearArgs& a, hipStream_t st);
+int32_t launch_linear_tile(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st);
 size_t act_grad_workspace_bytes(int E, int N, int rows);
 int32_t launch_act_grad(const void* dy, const void* pre, const void* mul, const int32_t* offsets, int E, int N,
                         int rows, int dtype, int act, void* dpre, void* dmul, float* dbias, float* part,

@@ -100,9 +100,7 @@ static void run_general(int mode, const LinearArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((linear_general_kernel<T, kDw>), dim3((unsigned)general_blocks<kDw>(a)), dim3(256), 0, st, a);
 }
 
-LinearPlan plan_linear(int, const LinearArgs&) { return {kPlanGeneral, 1, 0}; }
-
-int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan&, hipStream_t st) {
+int32_t launch_linear_general(int mode, int dtype, const LinearArgs& a, hipStream_t st) {
   if (dtype == MILO_F16) run_general<F16>(mode, a, st);
   else run_general<BF16>(mode, a, st);
   return hip_status(hipGetLastError(), "linear_general_kernel launch");

@@ -1,0 +1,264 @@
+// The grouped 16-bit product on the matrix cores: BM x BN output tiles, the
+// contraction in steps of 64 through LDS.  Needs row lengths of a multiple of
+// 8 elements and 16-byte aligned operands (the plan's rule); any row count.
+//
+// Operands go from memory straight into LDS, 16 bytes a lane, through buffer
+// resources that end where the operand does: what lies past a row range, a
+// column range or the contraction arrives as zeros.  Two LDS buffers: a step
+// computes on one while the next step's data arrives in the other.
+//
+// deep operand: LDS [row][64], 16-byte piece c of row r at place c ^ (r mod 8).
+//   A fragment (16 rows, 8 contraction values a lane) is one 16-byte LDS read;
+//   the places spread 8 rows over all banks.
+// wide operand: LDS [64][cols] as in memory, 32-byte granule g of contraction
+//   row k at place g ^ f(k).  A fragment is two transposing reads
+//   (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, lane i gets column
+//   i); f gives the rows of one read different banks.
+#pragma once
+
+#include "linear.hpp"
+
+namespace milo {
+
+constexpr int kDepth = 64;                 // contraction values per step
+constexpr int kTileRsrcWord3 = 0x00020000; // raw buffer, bounds checked in bytes
+constexpr int kOutside = 0x7FFFFFF0;       // an offset no operand reaches
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// ROWS rows (deep) or columns (wide) of one operand, staged by NW waves.
+template <bool WIDE, int ROWS, int NW>
+struct Operand {
+  static constexpr int kLoads = ROWS * kDepth * 2 / (16 * 64 * NW);   // per lane and step
+  static constexpr int kBytes = ROWS * kDepth * 2;
+  int voff[kLoads];      // byte offset of each piece from the step's first element
+  int piece[kLoads];     // deep: contraction index of the piece within the step
+
+  static __device__ __forceinline__ int wide_swizzle(int k) {
+    return ((k & 3) | (((k >> 3) & 3) << 2)) & (ROWS / 16 - 1);
+  }
+
+  // ld: elements between rows; cols_left: wide, columns from the tile's first to the operand's end
+  __device__ __forceinline__ void init(int lane, int wave, int ld, int cols_left) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int slot = (j * NW + wave) * 64 + lane;
+      if constexpr (!WIDE) {
+        const int r = slot >> 3, c = (slot & 7) ^ (r & 7);
+        voff[j] = r * ld * 2 + c * 16;
+        piece[j] = c * 8;
+      } else {
+        const int k = slot / (ROWS / 8), p = slot % (ROWS / 8);
+        const int c = (((p >> 1) ^ wide_swizzle(k)) << 1) | (p & 1);
+        voff[j] = c * 8 < cols_left ? k * ld * 2 + c * 16 : kOutside;
+        piece[j] = 0;
+      }
+    }
+  }
+
+  // Step k0 into LDS at dst.  deep: src is the tile's first row, `left` its
+  // rows inside the operand; wide: src is the tile's first column of the first
+  // contraction row, `depth` the contraction's length.
+  __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int left, int depth, int k0, char* dst,
+                                       int wave) const {
+    if constexpr (!WIDE) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(src + k0), 0, (int)(left * ld - k0) * 2, kTileRsrcWord3);
+      const bool whole = k0 + kDepth <= depth;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (j * NW + wave) * 1024), 16,
+                                                 whole || k0 + piece[j] < depth ? voff[j] : kOutside, 0, 0, 0);
+    } else {
+      const int rows = depth - k0 < kDepth ? depth - k0 : kDepth;
+      // `left` columns remain in the last row: the resource ends with the operand's last element
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(src + k0 * ld), 0, (int)((rows - 1) * ld + left) * 2, kTileRsrcWord3);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (j * NW + wave) * 1024), 16, voff[j], 0, 0, 0);
+    }
+  }
+};
+
+// Fragments of NF 16-wide groups starting at row (column) w0 of an LDS tile.
+template <bool WIDE, int ROWS, int NF>
+struct Fragments {
+  int off[WIDE ? NF : 2];
+  __device__ __forceinline__ void init(int lane, int w0) {
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        off[s] = (w0 + (lane & 15)) * kDepth * 2 + (((4 * s + (lane >> 4)) ^ (lane & 7)) << 4);
+    } else {
+      const int i = lane & 15, k = 8 * (lane >> 4) + (i >> 2);
+      const int f = ((k & 3) | (((k >> 3) & 3) << 2)) & (ROWS / 16 - 1);
+#pragma unroll
+      for (int t = 0; t < NF; ++t) off[t] = k * ROWS * 2 + (((w0 >> 4) + t) ^ f) * 32 + (i & 3) * 8;
+    }
+  }
+  // group t of the step's half s (32 contraction values)
+  __device__ __forceinline__ s16x8 read(const char* lds, int s, int t) const {
+    if constexpr (!WIDE) {
+      return *(const s16x8*)(lds + off[s] + t * 16 * kDepth * 2);
+    } else {
+      typedef __attribute__((address_space(3))) s16x4 lds4;
+      const char* p = lds + off[t] + s * 32 * ROWS * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * ROWS * 2));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// Block -> tile.  Blocks go to the 8 XCDs in turn; each XCD gets a run of
+// consecutive tiles, so that tiles sharing operands share its L2.
+__device__ __forceinline__ int xcd_order(int id, int total) {
+  const int q = total >> 3, r = total & 7, x = id & 7, i = id >> 3;
+  if (i >= q + (x < r ? 1 : 0)) return -1;
+  return x * q + (x < r ? x : r) + i;
+}
+
+// Within an expert: bands of kBand column tiles, row tiles inside a band.
+constexpr int kBand = 8;
+__device__ __forceinline__ void band_order(int local, int tm, int tn, int* m, int* n) {
+  const int band = local / (kBand * tm), first = band * kBand;
+  const int width = tn - first < kBand ? tn - first : kBand, rest = local - first * tm;
+  *m = rest / width;
+  *n = first + rest % width;
+}
+
+template <int BM, int BN>
+constexpr size_t tile_lds() {
+  return (size_t)2 * (BM + BN) * kDepth * 2;
+}
+
+template <class T, int MODE, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN) linear_tile_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
+  constexpr int NW = WM * WN, NI = BM / WM / 16, NJ = BN / WN / 16;
+  constexpr bool AW = MODE == kDw, BW = MODE != kFwd;
+  extern __shared__ __align__(16) char lds[];
+  typedef Operand<AW, BM, NW> OpA;
+  typedef Operand<BW, BN, NW> OpB;
+  constexpr int kBuf = OpA::kBytes + OpB::kBytes;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = MODE == kFwd ? a.N : a.K;
+  const int tn = (cols + BN - 1) / BN;
+  const int split = blockIdx.y;
+  TileSlot s;
+  int mt, nt;
+  if constexpr (MODE == kDw) {
+    const int tm = (a.N + BM - 1) / BM, id = xcd_order(blockIdx.x, a.E * tm * tn);
+    if (id < 0) return;
+    s.e = id / (tm * tn);
+    s.span = expert_span(a.offsets, s.e, a.rows);
+    band_order(id - s.e * tm * tn, tm, tn, &mt, &nt);
+  } else {
+    const int id = blockIdx.x;
+    s = find_slot(a.offsets, a.E, a.rows, BM, tn, [&](int total) { return xcd_order(id, total); });
+    if (s.e < 0) return;
+    band_order(s.local, s.row_tiles, tn, &mt, &nt);
+  }
+  const int m0 = mt * BM, n0 = nt * BN;
+  const int M = MODE == kDw ? a.N : s.span.rows;
+  const int D = MODE == kFwd ? a.K : MODE == kDx ? a.N : s.span.rows;
+  const int64_t lda = MODE == kFwd ? a.K : a.N, ldb = a.K;
+  const uint16_t* pa = (const uint16_t*)a.a + (int64_t)s.span.base * lda + (AW ? (int64_t)m0 : m0 * lda);
+  const uint16_t* pb = (const uint16_t*)a.b +
+                       (MODE == kDw ? (int64_t)s.span.base * ldb : (int64_t)s.e * a.N * a.K) +
+                       (BW ? (int64_t)n0 : n0 * ldb);
+  const int lefta = M - m0 < BM && !AW ? M - m0 : AW ? M - m0 : BM;
+  const int leftb = BW ? cols - n0 : cols - n0 < BN ? cols - n0 : BN;
+
+  OpA oa;
+  OpB ob;
+  oa.init(lane, wave, (int)lda, M - m0);
+  ob.init(lane, wave, (int)ldb, cols - n0);
+  const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+  Fragments<AW, BM, NI> fa;
+  Fragments<BW, BN, NJ> fb;
+  fa.init(lane, wm);
+  fb.init(lane, wn);
+  f32x4 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // this split's steps
+  const int all = (D + kDepth - 1) / kDepth, each = (all + a.splits - 1) / a.splits;
+  const int first = split * each, last = first + each < all ? first + each : all;
+  auto issue = [&](int k, int buf) {
+    char* dst = lds + buf * kBuf;
+    oa.load(pa, lda, lefta, D, k * kDepth, dst, wave);
+    ob.load(pb, ldb, leftb, D, k * kDepth, dst + OpA::kBytes, wave);
+  };
+  auto products = [&](int buf) {
+    const char* la = lds + buf * kBuf;
+    const char* lb = la + OpA::kBytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s16x8 xa[NI], xb[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) xb[j] = fb.read(lb, h, j);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) xa[i] = fa.read(la, h, i);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = T::mfma(xb[j], xa[i], acc[i][j]);
+    }
+  };
+  if (first < last) {
+    issue(first, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int k = first; k < last; ++k, buf ^= 1) {
+      if (k + 1 < last) issue(k + 1, buf ^ 1);
+      products(buf);
+      __syncthreads();
+    }
+  }
+
+  // Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each 16 x 16 product.
+  // Each wave turns 64 x 64 results at a time around in its own 16 KB of LDS
+  // (16-byte piece c of row r at place c ^ (r mod 16)), so that a lane gets 8
+  // consecutive columns: 128-byte rows of 16-byte accesses, one copy of the
+  // epilogue's code.
+  static_assert(NJ == 4 && NI % 4 == 0 && tile_lds<BM, BN>() >= (size_t)NW * 16384, "epilogue staging");
+  char* mine = lds + wave * 16384;
+#pragma unroll
+  for (int q = 0; q < NI / 4; ++q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = lane & 15;
+        *(f32x4*)(mine + (16 * i + r) * 256 + (((4 * j + (lane >> 4)) ^ r) << 4)) = acc[4 * q + i][j];
+      }
+    const int n = n0 + wn + 8 * (lane & 7);
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+      const int r = 8 * it + (lane >> 3), m = m0 + wm + 64 * q + r;
+      const int p = 2 * (lane & 7);
+      const f32x4 lo = *(const f32x4*)(mine + r * 256 + ((p ^ (r & 15)) << 4));
+      const f32x4 hi = *(const f32x4*)(mine + r * 256 + (((p + 1) ^ (r & 15)) << 4));
+      if (m >= M || n >= cols) continue;
+      const int64_t row = (MODE == kDw ? 0 : s.span.base) + (int64_t)m;
+      if (a.splits > 1) {
+        const int64_t rows = MODE == kDw ? (int64_t)a.E * a.N : a.rows;
+        float* part = a.part + (split * rows + (MODE == kDw ? (int64_t)s.e * a.N : 0) + row) * cols + n;
+        *(f32x4*)part = lo;
+        *(f32x4*)(part + 4) = hi;
+      } else {
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        finish<T, MODE, 8>(a, s.e, row, n, v);
+      }
+    }
+  }
+#endif
+}
+
+}  // namespace milo
