@@ -1,0 +1,125 @@
+// The grouped 16-bit product for few rows an expert (decoding): bound by
+// streaming the weights once.  A block takes 16 NT weight rows (output
+// columns) of one expert; its waves share the contraction, each walking it in
+// pieces of 128 with the next piece's loads in flight, straight from memory
+// into matrix-core operands (no LDS on the way: a weight is used once).  Row
+// counts up to 16 MT go in one walk; more rows walk again, 16 MT at a time.
+// Partial sums meet in LDS in wave order.
+//
+// A lane's operand: row l % 16, contraction values 8 (l / 16) .. +7 of a step
+// of 32: 16-byte loads, 64 contiguous bytes a row and load, four loads to 256.
+// Rows of x past the expert's and columns past N are cut off by the buffer
+// resources' ends: they read as zeros and cost no traffic.
+#include "linear.hpp"
+
+namespace milo {
+
+constexpr int kFewRsrcWord3 = 0x00020000;
+constexpr int kFewOutside = 0x7FFFFFF0;
+constexpr int kFewPiece = 128;            // contraction values a wave takes at a time
+
+template <class T, int MT, int NT, int NW>
+__device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, int m0, int rows, int n0, float* lds) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = a.K, left_n = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT;
+  const int left_m = rows - m0 < 16 * MT ? rows - m0 : 16 * MT;
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((const uint16_t*)a.b + ((int64_t)e * a.N + n0) * K), 0, left_n * K * 2, kFewRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((const uint16_t*)a.a + (int64_t)(base + m0) * K), 0, left_m * K * 2, kFewRsrcWord3);
+  const int at = (lane & 15) * K * 2 + (lane >> 4) * 16;   // byte offset of the lane's first piece
+  f32x4 acc[MT][NT] = {};
+  struct Piece {
+    u32x4 w[NT][4], x[MT][4];
+  };
+  auto load = [&](int k0, Piece& p) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bool in = k0 + 32 * s + 8 * (lane >> 4) < K;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        p.w[t][s] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? at + (16 * t * K + k0 + 32 * s) * 2 : kFewOutside, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        p.x[t][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? at + (16 * t * K + k0 + 32 * s) * 2 : kFewOutside, 0, 0);
+    }
+  };
+  auto use = [&](const Piece& p) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = T::mfma(__builtin_bit_cast(s16x8, p.w[j][s]), __builtin_bit_cast(s16x8, p.x[i][s]), acc[i][j]);
+  };
+  constexpr int kTurn = kFewPiece * NW;
+  Piece p0, p1;
+  const int first = wave * kFewPiece;
+  load(first, p0);
+  for (int k = first; k < K; k += 2 * kTurn) {      // loads past K are cut off: zeros
+    load(k + kTurn, p1);
+    use(p0);
+    load(k + 2 * kTurn, p0);
+    use(p1);
+  }
+  // partial sums: lds[wave][row][16 NT columns]; lane l holds row l % 16,
+  // columns 4 (l / 16) .. +3 of each product
+  constexpr int kLine = 16 * NT + 4;
+  __syncthreads();                                   // the previous walk's readers are done
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *(f32x4*)(lds + (wave * 16 * MT + 16 * i + (lane & 15)) * kLine + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < 16 * MT * 4 * NT; q += 64 * NW) {
+    const int r = q / (4 * NT), c = q % (4 * NT) * 4;
+    if (m0 + r >= rows || n0 + c >= a.N) continue;
+    f32x4 sum = *(const f32x4*)(lds + r * kLine + c);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += *(const f32x4*)(lds + (w * 16 * MT + r) * kLine + c);
+    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    finish<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, v);
+  }
+}
+
+// MT_MAX bounds the 16-row groups of one walk; an expert with fewer rows takes
+// the smallest form that holds them.
+template <class T, int MT_MAX, int NT, int NW>
+__global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(16) float lds[NW * 16 * MT_MAX * (16 * NT + 4)];
+  const int e = blockIdx.y, n0 = blockIdx.x * 16 * NT;
+  const Span s = expert_span(a.offsets, e, a.rows);
+  for (int m0 = 0; m0 < s.rows; m0 += 16 * MT_MAX) {
+    const int left = s.rows - m0;
+    if (left <= 16 || MT_MAX == 1) few_rows<T, 1, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
+    else if (left <= 32 || MT_MAX == 2) few_rows<T, MT_MAX < 2 ? 1 : 2, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
+    else few_rows<T, MT_MAX, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
+  }
+#endif
+}
+
+template <class T>
+static void run_few(const LinearArgs& a, hipStream_t st) {
+  // two column groups a block halve the traffic of x; with few columns in all
+  // one group and eight waves spread the weights over more of the chip
+  const int64_t groups = (int64_t)a.E * ((a.N + 31) / 32);
+  const bool wide = groups >= 1024;
+#define RUN(MT, NT, NW)                                                                                        \
+  hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E), dim3(64 * NW), \
+                     0, st, a)
+  if (a.max_rows <= 16) { if (wide) RUN(1, 2, 4); else RUN(1, 1, 8); }
+  else if (a.max_rows <= 32) { if (wide) RUN(2, 2, 4); else RUN(2, 1, 8); }
+  else { if (wide) RUN(4, 2, 4); else RUN(4, 1, 8); }
+#undef RUN
+}
+
+int32_t launch_linear_few(int dtype, const LinearArgs& a, hipStream_t st) {
+  if (dtype == MILO_F16) run_few<F16>(a, st);
+  else run_few<BF16>(a, st);
+  return hip_status(hipGetLastError(), "linear_few_kernel launch");
+}
+
+}  // namespace milo
