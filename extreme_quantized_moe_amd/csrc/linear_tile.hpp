@@ -56,14 +56,15 @@ struct Operand {
     }
   }
 
-  // Step k0 into LDS at dst.  deep: src is the tile's first row, `left` its
-  // rows inside the operand; wide: src is the tile's first column of the first
-  // contraction row, `depth` the contraction's length.
-  __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int left, int depth, int k0, char* dst,
-                                       int wave) const {
+  // Step k0 into LDS at dst; nothing (zeros, no traffic) unless `on`.  deep:
+  // src is the tile's first row, `left` its rows inside the operand; wide: src
+  // is the tile's first column of the first contraction row, `depth` the
+  // contraction's length.  No branch: the loads are spread between products.
+  __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int left, int depth, int k0, bool on,
+                                       char* dst, int wave) const {
     if constexpr (!WIDE) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(src + k0), 0, (int)(left * ld - k0) * 2, kTileRsrcWord3);
+          (void*)(src + k0), 0, on ? (int)(left * ld - k0) * 2 : 0, kTileRsrcWord3);
       const bool whole = k0 + kDepth <= depth;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
@@ -73,7 +74,7 @@ struct Operand {
       const int rows = depth - k0 < kDepth ? depth - k0 : kDepth;
       // `left` columns remain in the last row: the resource ends with the operand's last element
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(src + k0 * ld), 0, (int)((rows - 1) * ld + left) * 2, kTileRsrcWord3);
+          (void*)(src + k0 * ld), 0, on ? (int)((rows - 1) * ld + left) * 2 : 0, kTileRsrcWord3);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (j * NW + wave) * 1024), 16, voff[j], 0, 0, 0);
@@ -133,8 +134,36 @@ constexpr size_t tile_lds() {
   return (size_t)2 * (BM + BN) * kDepth * 2;
 }
 
+// Scheduling of one half step: its LDS reads and loads spread evenly between
+// its products, so that the matrix cores never wait for the LDS or the loads'
+// issue.
+template <int MFMAS, int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kGroups = 16, kM = MFMAS / kGroups;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    constexpr int kR = READS / kGroups, kL = LOADS / kGroups;
+    if constexpr (kR > 0) __builtin_amdgcn_sched_group_barrier(0x100, kR, 0);
+    else if (g < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, kM, 0);
+    if constexpr (kL > 0) __builtin_amdgcn_sched_group_barrier(0x020, kL, 0);
+    else if (g < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+  }
+#endif
+}
+
+// Every wave's loads into LDS have arrived and its LDS reads are done.  The
+// barrier alone does not wait for loads into LDS: the wait is explicit.
+__device__ __forceinline__ void arrived() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#endif
+  __syncthreads();
+}
+
 template <class T, int MODE, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN) linear_tile_kernel(LinearArgs a) {
+__global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
   constexpr int NW = WM * WN, NI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr bool AW = MODE == kDw, BW = MODE != kFwd;
@@ -187,39 +216,51 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_tile_kernel(LinearArgs a)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // this split's steps
+  // This split's steps.  Step k is used in two halves of 32 contraction
+  // values; the fragments of one half are read from LDS while the products of
+  // the half before run.  One barrier a step, between the halves: there every
+  // wave has read the last of buffer k (so step k + 2 may be loaded into it,
+  // a whole step of products ahead of its use) and its part of step k + 1 has
+  // arrived.
   const int all = (D + kDepth - 1) / kDepth, each = (all + a.splits - 1) / a.splits;
   const int first = split * each, last = first + each < all ? first + each : all;
   auto issue = [&](int k, int buf) {
     char* dst = lds + buf * kBuf;
-    oa.load(pa, lda, lefta, D, k * kDepth, dst, wave);
-    ob.load(pb, ldb, leftb, D, k * kDepth, dst + OpA::kBytes, wave);
+    oa.load(pa, lda, lefta, D, k * kDepth, k < last, dst, wave);
+    ob.load(pb, ldb, leftb, D, k * kDepth, k < last, dst + OpA::kBytes, wave);
   };
-  auto products = [&](int buf) {
+  s16x8 xa[2][NI], xb[2][NJ];
+  auto read = [&](int buf, int h) {
     const char* la = lds + buf * kBuf;
-    const char* lb = la + OpA::kBytes;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s16x8 xa[NI], xb[NJ];
+    for (int j = 0; j < NJ; ++j) xb[h][j] = fb.read(la + OpA::kBytes, h, j);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) xb[j] = fb.read(lb, h, j);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) xa[i] = fa.read(la, h, i);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = T::mfma(xb[j], xa[i], acc[i][j]);
-    }
+    for (int i = 0; i < NI; ++i) xa[h][i] = fa.read(la, h, i);
   };
+  auto products = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = T::mfma(xb[h][j], xa[h][i], acc[i][j]);
+  };
+  constexpr int kReads = NI * (AW ? 2 : 1) + NJ * (BW ? 2 : 1), kLoads = OpA::kLoads + OpB::kLoads;
   if (first < last) {
     issue(first, 0);
-    __syncthreads();
+    issue(first + 1, 1);
+    arrived();
+    read(0, 0);
     int buf = 0;
     for (int k = first; k < last; ++k, buf ^= 1) {
-      if (k + 1 < last) issue(k + 1, buf ^ 1);
-      products(buf);
-      __syncthreads();
+      read(buf, 1);
+      products(0);
+      interleave<NI * NJ, kReads, 0>();
+      arrived();
+      issue(k + 2, buf);
+      read(buf ^ 1, 0);          // past the last step: stale data, never used
+      products(1);
+      interleave<NI * NJ, kReads, kLoads>();
     }
+    arrived();             // the epilogue reuses the LDS
   }
 
   // Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each 16 x 16 product.
@@ -227,18 +268,19 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_tile_kernel(LinearArgs a)
   // (16-byte piece c of row r at place c ^ (r mod 16)), so that a lane gets 8
   // consecutive columns: 128-byte rows of 16-byte accesses, one copy of the
   // epilogue's code.
-  static_assert(NJ == 4 && NI % 4 == 0 && tile_lds<BM, BN>() >= (size_t)NW * 16384, "epilogue staging");
+  static_assert(NJ % 4 == 0 && NI % 4 == 0 && tile_lds<BM, BN>() >= (size_t)NW * 16384, "epilogue staging");
   char* mine = lds + wave * 16384;
 #pragma unroll
-  for (int q = 0; q < NI / 4; ++q) {
+  for (int qq = 0; qq < NI / 4 * (NJ / 4); ++qq) {
+    const int q = qq / (NJ / 4), g = qq % (NJ / 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = lane & 15;
-        *(f32x4*)(mine + (16 * i + r) * 256 + (((4 * j + (lane >> 4)) ^ r) << 4)) = acc[4 * q + i][j];
+        *(f32x4*)(mine + (16 * i + r) * 256 + (((4 * j + (lane >> 4)) ^ r) << 4)) = acc[4 * q + i][4 * g + j];
       }
-    const int n = n0 + wn + 8 * (lane & 7);
+    const int n = n0 + wn + 64 * g + 8 * (lane & 7);
 #pragma unroll 1
     for (int it = 0; it < 8; ++it) {
       const int r = 8 * it + (lane >> 3), m = m0 + wm + 64 * q + r;
