@@ -116,52 +116,96 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offset
 }
 
 // ---------------------------------------------------------------- activations
-// Float32 values; the tails are computed without cancellation (erfc, sigmoid)
-// so that they are right to float32 relative precision, and arguments are
-// bounded where a product of 0 and infinity would appear.  NaN stays NaN.
+// Float32 values, a few instructions each: in the tile kernel's epilogue and in
+// the activation gradient they run once per output on the vector units, 16
+// lanes a cycle, with nothing else to hide behind.  Tails are computed without
+// cancellation (sigmoid from exp(-|v|), the normal distribution from erfcx), so
+// they hold float32 relative precision down to results of 2^-126, which the
+// exponential flushes to zero.  Arguments are bounded where a product of 0 and
+// infinity would appear.  NaN stays NaN.
 __device__ __forceinline__ float bounded(float v, float lo, float hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// From exp(-|v|), which never overflows: far negative tails keep their value
-// down to the smallest float32.
-__device__ __forceinline__ float sigmoid(float v) {
-  const float e = expf(-__builtin_fabsf(v));
-  return (v < 0.f ? e : 1.f) / (1.f + e);
-}
-
-constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhC = 0.79788456080286536f;       // sqrt(2 / pi)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+__device__ __forceinline__ float exp2_fast(float v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return __builtin_amdgcn_exp2f(v);
+#else
+  return v;
+#endif
+}
+
+__device__ __forceinline__ float rcp_fast(float v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return __builtin_amdgcn_rcpf(v);
+#else
+  return v;
+#endif
+}
+
+__device__ __forceinline__ float sigmoid(float v) {
+  const float e = exp2_fast(-kLog2e * __builtin_fabsf(v));
+  return (v < 0.f ? e : 1.f) * rcp_fast(1.f + e);
+}
+
+// Phi(v) of the normal distribution, and exp(-v^2 / 2).  With z = |v| / sqrt 2
+// and t = 1 / (1 + z / 2): erfc(z) = exp(-z^2) erfcx(z), erfcx(z) / t a
+// polynomial of degree 8 in t fitted for the smallest largest relative error
+// on z <= 14 (4.5e-8; 1.3e-7 in float32), beyond which exp(-z^2) is zero.
+__device__ __forceinline__ float normal_cdf(float v, float* exp_half_sq) {
+  const float s = v * v, lo = __builtin_fmaf(v, v, -s);      // v^2 to twice the precision
+  const float e = exp2_fast(__builtin_fmaf(s, -0.5f * kLog2e, lo * (-0.5f * kLog2e)));
+  const float t = rcp_fast(__builtin_fmaf(__builtin_fabsf(v), 0.35355339059327376f, 1.f));
+  float p = -0.05938772112131119f;
+  p = __builtin_fmaf(p, t, 0.28612956404685974f);
+  p = __builtin_fmaf(p, t, -0.49041667580604553f);
+  p = __builtin_fmaf(p, t, 0.28174346685409546f);
+  p = __builtin_fmaf(p, t, -0.029154308140277863f);
+  p = __builtin_fmaf(p, t, 0.20375439524650574f);
+  p = __builtin_fmaf(p, t, 0.24283479154109955f);
+  p = __builtin_fmaf(p, t, 0.2824121117591858f);
+  p = __builtin_fmaf(p, t, 0.2820843458175659f);
+  const float h = 0.5f * e * (t * p);
+  *exp_half_sq = e;
+  return v < 0.f ? h : 1.f - h;
+}
+
+__device__ __forceinline__ float tanh_gelu_arg(float v) {
+  return 2.f * kTanhC * __builtin_fmaf(0.044715f * v * v, v, v);
+}
+
 __device__ __forceinline__ float act_value(int act, float v) {
+  float e;
   switch (act) {
     case MILO_ACT_RELU: return v < 0.f ? 0.f : v;
     case MILO_ACT_SILU: v = v < -1e3f ? -1e3f : v; return v * sigmoid(v);
-    case MILO_ACT_GELU: v = v < -1e3f ? -1e3f : v; return 0.5f * v * erfcf(-v * kSqrtHalf);
-    case MILO_ACT_GELU_TANH:
-      v = v < -1e3f ? -1e3f : v;
-      return v * sigmoid(2.f * kTanhC * __builtin_fmaf(0.044715f * v * v, v, v));
+    case MILO_ACT_GELU: v = v < -1e3f ? -1e3f : v; return v * normal_cdf(bounded(v, -1e3f, 1e3f), &e);
+    case MILO_ACT_GELU_TANH: v = v < -1e3f ? -1e3f : v; return v * sigmoid(tanh_gelu_arg(bounded(v, -1e3f, 1e3f)));
     default: return v;
   }
 }
 
 // act(v) and act'(v); relu'(0) = 0.
 __device__ __forceinline__ float act_slope(int act, float v, float* value) {
+  const float b = bounded(v, -1e3f, 1e3f), w = v > b ? v : b;
   switch (act) {
     case MILO_ACT_RELU: *value = v < 0.f ? 0.f : v; return v > 0.f ? 1.f : v <= 0.f ? 0.f : v;
     case MILO_ACT_SILU: {
-      const float b = bounded(v, -1e3f, 1e3f), g = sigmoid(b);
-      *value = (v > b ? v : b) * g;
+      const float g = sigmoid(b);
+      *value = w * g;
       return g * __builtin_fmaf(b, 1.f - g, 1.f);
     }
     case MILO_ACT_GELU: {
-      const float b = bounded(v, -1e3f, 1e3f), cdf = 0.5f * erfcf(-b * kSqrtHalf);
-      *value = (v > b ? v : b) * cdf;
-      return __builtin_fmaf(b * kInvSqrt2Pi, expf(-0.5f * b * b), cdf);
+      float e;
+      const float cdf = normal_cdf(b, &e);
+      *value = w * cdf;
+      return __builtin_fmaf(b * kInvSqrt2Pi, e, cdf);
     }
     case MILO_ACT_GELU_TANH: {
-      const float b = bounded(v, -1e3f, 1e3f);
-      const float g = sigmoid(2.f * kTanhC * __builtin_fmaf(0.044715f * b * b, b, b));
-      *value = (v > b ? v : b) * g;
+      const float g = sigmoid(tanh_gelu_arg(b));
+      *value = w * g;
       // d/dv of v g(2 u), u' = c (1 + 3 0.044715 v^2)
       return __builtin_fmaf(b * g * (1.f - g), 2.f * kTanhC * __builtin_fmaf(3.f * 0.044715f * b, b, 1.f), g);
     }
@@ -174,41 +218,38 @@ __device__ __forceinline__ float act_slope(int act, float v, float* value) {
 // address to allow V-wide accesses (the launcher's rule).  Forward: bias, the
 // kept pre-activation, activation, gate operand, residual, all in float32,
 // one rounding at each store.
-template <class T, int MODE, int V>
-__device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, int col, const float* v_in) {
-  const int ld = MODE == kFwd ? a.N : a.K;
-  const int64_t at = (MODE == kDw ? ((int64_t)e * a.N + row) : row) * ld + col;
-  float v[V];
+template <int MODE>
+__device__ __forceinline__ int64_t out_at(const LinearArgs& a, int e, int64_t row, int col) {
+  return ((MODE == kDw ? (int64_t)e * a.N : 0) + row) * (MODE == kFwd ? a.N : a.K) + col;
+}
+
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const void* p, int64_t at) {
+  return *(const Pack<T, V>*)((const uint16_t*)p + at);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void add_pack(float* v, const Pack<T, V>& p) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = v_in[i];
-  if constexpr (MODE == kFwd) {
-    typedef Pack<T, V> P;
-    if (a.bias) {
-      const P b = *(const P*)((const uint16_t*)a.bias + (int64_t)e * ld + col);
+  for (int i = 0; i < V; ++i) v[i] += T::up(p.v[i]);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void mul_pack(float* v, const Pack<T, V>& p) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += T::up(b.v[i]);
-    }
-    if (a.pre) {
-      P p;
+  for (int i = 0; i < V; ++i) v[i] *= T::up(p.v[i]);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_pack(void* dst, int64_t at, const float* v) {
+  Pack<T, V> o;
 #pragma unroll
-      for (int i = 0; i < V; ++i) p.v[i] = T::down(v[i]);
-      *(P*)((uint16_t*)a.pre + at) = p;
-    }
-    if (a.act != MILO_ACT_NONE) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_value(a.act, v[i]);
-    }
-    if (a.mul) {
-      const P m = *(const P*)((const uint16_t*)a.mul + at);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= T::up(m.v[i]);
-    }
-  }
-  if (MODE != kDw && a.residual) {
-    const Pack<T, V> r = *(const Pack<T, V>*)((const uint16_t*)a.residual + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += T::up(r.v[i]);
-  }
+  for (int i = 0; i < V; ++i) o.v[i] = T::down(v[i]);
+  *(Pack<T, V>*)((uint16_t*)dst + at) = o;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_out(const LinearArgs& a, int64_t at, const float* v) {
   if (a.out_f32) {
     constexpr int W = V < 4 ? V : 4;        // at most 16 bytes an access
 #pragma unroll
@@ -219,11 +260,27 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, 
       *(Pack<F32, W>*)((float*)a.out + at + p * W) = o;
     }
   } else {
-    Pack<T, V> o;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = T::down(v[i]);
-    *(Pack<T, V>*)((uint16_t*)a.out + at) = o;
+    store_pack<T, V>(a.out, at, v);
   }
+}
+
+template <class T, int MODE, int V>
+__device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, int col, const float* v_in) {
+  const int64_t at = out_at<MODE>(a, e, row, col);
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = v_in[i];
+  if constexpr (MODE == kFwd) {
+    if (a.bias) add_pack<T, V>(v, load_pack<T, V>(a.bias, (int64_t)e * a.N + col));
+    if (a.pre) store_pack<T, V>(a.pre, at, v);
+    if (a.act != MILO_ACT_NONE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_value(a.act, v[i]);
+    }
+    if (a.mul) mul_pack<T, V>(v, load_pack<T, V>(a.mul, at));
+  }
+  if (MODE != kDw && a.residual) add_pack<T, V>(v, load_pack<T, V>(a.residual, at));
+  store_out<T, V>(a, at, v);
 }
 
 // ---------------------------------------------------------------- host side

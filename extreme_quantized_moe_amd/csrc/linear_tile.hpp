@@ -162,35 +162,18 @@ __device__ __forceinline__ void arrived() {
   __syncthreads();
 }
 
+// One tile: rows m0 .. of the expert's span (or output rows of dw), columns
+// n0 .., this split's share of the contraction.
 template <class T, int MODE, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
+__device__ __forceinline__ void tile_body(const LinearArgs& a, const TileSlot& s, int m0, int n0, int split,
+                                          char* lds) {
   constexpr int NW = WM * WN, NI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr bool AW = MODE == kDw, BW = MODE != kFwd;
-  extern __shared__ __align__(16) char lds[];
   typedef Operand<AW, BM, NW> OpA;
   typedef Operand<BW, BN, NW> OpB;
   constexpr int kBuf = OpA::kBytes + OpB::kBytes;
-
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = MODE == kFwd ? a.N : a.K;
-  const int tn = (cols + BN - 1) / BN;
-  const int split = blockIdx.y;
-  TileSlot s;
-  int mt, nt;
-  if constexpr (MODE == kDw) {
-    const int tm = (a.N + BM - 1) / BM, id = xcd_order(blockIdx.x, a.E * tm * tn);
-    if (id < 0) return;
-    s.e = id / (tm * tn);
-    s.span = expert_span(a.offsets, s.e, a.rows);
-    band_order(id - s.e * tm * tn, tm, tn, &mt, &nt);
-  } else {
-    const int id = blockIdx.x;
-    s = find_slot(a.offsets, a.E, a.rows, BM, tn, [&](int total) { return xcd_order(id, total); });
-    if (s.e < 0) return;
-    band_order(s.local, s.row_tiles, tn, &mt, &nt);
-  }
-  const int m0 = mt * BM, n0 = nt * BN;
   const int M = MODE == kDw ? a.N : s.span.rows;
   const int D = MODE == kFwd ? a.K : MODE == kDx ? a.N : s.span.rows;
   const int64_t lda = MODE == kFwd ? a.K : a.N, ldb = a.K;
@@ -266,9 +249,8 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   // Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each 16 x 16 product.
   // Each wave turns 64 x 64 results at a time around in its own 16 KB of LDS
   // (16-byte piece c of row r at place c ^ (r mod 16)), so that a lane gets 8
-  // consecutive columns: 128-byte rows of 16-byte accesses, one copy of the
-  // epilogue's code.
-  static_assert(NJ % 4 == 0 && NI % 4 == 0 && tile_lds<BM, BN>() >= (size_t)NW * 16384, "epilogue staging");
+  // consecutive columns: 128-byte rows of 16-byte accesses.
+  static_assert(NJ % 4 == 0 && NI % 4 == 0, "the epilogue takes 64 x 64 results at a time");
   char* mine = lds + wave * 16384;
 #pragma unroll
   for (int qq = 0; qq < NI / 4 * (NJ / 4); ++qq) {
@@ -280,26 +262,103 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
         const int r = lane & 15;
         *(f32x4*)(mine + (16 * i + r) * 256 + (((4 * j + (lane >> 4)) ^ r) << 4)) = acc[4 * q + i][4 * g + j];
       }
-    const int n = n0 + wn + 64 * g + 8 * (lane & 7);
+    const int n = n0 + wn + 64 * g + 8 * (lane & 7), mq = m0 + wm + 64 * q + (lane >> 3);
+    const int64_t row = (MODE == kDw ? 0 : s.span.base) + (int64_t)mq;
+    // step it of a pass: row mq + 8 it, its two 16-byte pieces
+    auto lo_at = [&](int it) {
+      const int r = 8 * it + (lane >> 3);
+      return (f32x4*)(mine + r * 256 + (((2 * (lane & 7)) ^ (r & 15)) << 4));
+    };
+    auto hi_at = [&](int it) {
+      const int r = 8 * it + (lane >> 3);
+      return (f32x4*)(mine + r * 256 + (((2 * (lane & 7) + 1) ^ (r & 15)) << 4));
+    };
+    if (a.splits > 1) {
+      const int64_t rows = MODE == kDw ? (int64_t)a.E * a.N : a.rows;
+      float* part = a.part + (split * rows + (MODE == kDw ? (int64_t)s.e * a.N : 0) + row) * cols + n;
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+        if (mq + 8 * it < M && n < cols) {
+          *(f32x4*)(part + (int64_t)8 * it * cols) = *lo_at(it);
+          *(f32x4*)(part + (int64_t)8 * it * cols + 4) = *hi_at(it);
+        }
+      continue;
+    }
+    // What the epilogue reads is asked for before the first pass: its latency
+    // is paid once for the 64 x 64 results, not once a row.
+    const bool has_mul = MODE == kFwd && a.mul, has_add = MODE != kDw && a.residual;
+    Pack<T, 8> bias = {}, mul[8], add[8];
+    if (MODE == kFwd && a.bias && n < cols) bias = load_pack<T, 8>(a.bias, (int64_t)s.e * a.N + n);
+    if (has_mul) {
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+        if (mq + 8 * it < M && n < cols) mul[it] = load_pack<T, 8>(a.mul, (row + 8 * it) * cols + n);
+    }
+    if (has_add) {
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+        if (mq + 8 * it < M && n < cols) add[it] = load_pack<T, 8>(a.residual, (row + 8 * it) * cols + n);
+    }
+    if (MODE == kFwd && (a.bias || a.pre || a.act != MILO_ACT_NONE)) {
+      // bias, kept pre-activation and activation, back into LDS: one copy of
+      // the activations' code
 #pragma unroll 1
-    for (int it = 0; it < 8; ++it) {
-      const int r = 8 * it + (lane >> 3), m = m0 + wm + 64 * q + r;
-      const int p = 2 * (lane & 7);
-      const f32x4 lo = *(const f32x4*)(mine + r * 256 + ((p ^ (r & 15)) << 4));
-      const f32x4 hi = *(const f32x4*)(mine + r * 256 + (((p + 1) ^ (r & 15)) << 4));
-      if (m >= M || n >= cols) continue;
-      const int64_t row = (MODE == kDw ? 0 : s.span.base) + (int64_t)m;
-      if (a.splits > 1) {
-        const int64_t rows = MODE == kDw ? (int64_t)a.E * a.N : a.rows;
-        float* part = a.part + (split * rows + (MODE == kDw ? (int64_t)s.e * a.N : 0) + row) * cols + n;
-        *(f32x4*)part = lo;
-        *(f32x4*)(part + 4) = hi;
-      } else {
-        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        finish<T, MODE, 8>(a, s.e, row, n, v);
+      for (int it = 0; it < 8; ++it) {
+        if (mq + 8 * it >= M || n >= cols) continue;
+        const f32x4 lo = *lo_at(it), hi = *hi_at(it);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if (a.bias) add_pack<T, 8>(v, bias);
+        if (a.pre) store_pack<T, 8>(a.pre, (row + 8 * it) * cols + n, v);
+        if (a.act != MILO_ACT_NONE) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = act_value(a.act, v[i]);
+        }
+        *lo_at(it) = f32x4{v[0], v[1], v[2], v[3]};
+        *hi_at(it) = f32x4{v[4], v[5], v[6], v[7]};
       }
     }
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      if (mq + 8 * it >= M || n >= cols) continue;
+      const f32x4 lo = *lo_at(it), hi = *hi_at(it);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (has_mul) mul_pack<T, 8>(v, mul[it]);
+      if (has_add) add_pack<T, 8>(v, add[it]);
+      store_out<T, 8>(a, out_at<MODE>(a, s.e, row + 8 * it, n), v);
+    }
   }
+}
+
+// A row tile with at most half of its rows runs a form of half the height (a
+// quarter of the experts' last tiles otherwise multiply mostly nothing).
+template <class T, int MODE, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
+  extern __shared__ __align__(16) char lds[];
+  static_assert(tile_lds<BM, BN>() >= (size_t)WM * WN * 16384, "the epilogue's staging fits");
+  const int tn = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
+  TileSlot s;
+  int mt, nt;
+  if constexpr (MODE == kDw) {
+    const int tm = (a.N + BM - 1) / BM, id = xcd_order(blockIdx.x, a.E * tm * tn);
+    if (id < 0) return;
+    s.e = id / (tm * tn);
+    s.span = expert_span(a.offsets, s.e, a.rows);
+    band_order(id - s.e * tm * tn, tm, tn, &mt, &nt);
+  } else {
+    const int id = blockIdx.x;
+    s = find_slot(a.offsets, a.E, a.rows, BM, tn, [&](int total) { return xcd_order(id, total); });
+    if (s.e < 0) return;
+    band_order(s.local, s.row_tiles, tn, &mt, &nt);
+  }
+  const int m0 = mt * BM, left = (MODE == kDw ? a.N : s.span.rows) - m0;
+  if constexpr (BM == 256) {
+    if (left <= BM / 2) {
+      tile_body<T, MODE, BM / 2, BN, WM, WN>(a, s, m0, nt * BN, blockIdx.y, lds);
+      return;
+    }
+  }
+  tile_body<T, MODE, BM, BN, WM, WN>(a, s, m0, nt * BN, blockIdx.y, lds);
 #endif
 }
 

@@ -5,7 +5,13 @@ Bounds, per element: u = half a rounding step of the output type relative to
 the value (bf16 2^-8 / 2 ... stated as `torch.finfo(t).eps / 2`), plus the
 smallest subnormal step for fp16 (values under its normal range), plus float32
 work: a sum of n products rounds at most n times, each by 2^-24 of the partial
-sum, which the sum of absolute products bounds."""
+sum, which the sum of absolute products bounds.
+
+Far tails: the activations are v g and slopes g (1 + ...) with g = c exp(-s),
+c <= 1, in float32.  The hardware's exponential returns 0 for results under
+2^-126, so g may lose up to 2^-126 there and nowhere else, and what multiplies g
+bounds the loss: |v| for the value, (1 + |v|) 2 (1 + v^2) for the slope (the
+widest, GELU_TANH: 1 + v (1 - g) 2 sqrt(2/pi) (1 + 0.134 v^2))."""
 import math
 
 import torch
@@ -26,6 +32,17 @@ def tiny(t):
 def rounded(value, t):
     """How far one rounding to t can be from `value`."""
     return value.abs() * half_step(t) + tiny(t)
+
+
+FLUSH = 2.0 ** -126
+
+
+def lost_value(v):
+    return FLUSH * v.abs()
+
+
+def lost_slope(v):
+    return FLUSH * (1 + v.abs()) * 2 * (1 + v * v)
 
 
 def act(name, v):
@@ -93,7 +110,7 @@ def linear_ref(x, w, offsets, bias, name, mul, res):
     y = act(name, pre)
     # slopes stay under 1.13; the float32 activation itself is good to a few
     # tens of roundings (exp of a rounded argument up to ~100: 2^-24 * 100)
-    err = 1.13 * pre_err + (0 if name in ("none", "relu") else 128 * U32 * y.abs())
+    err = 1.13 * pre_err + (0 if name in ("none", "relu") else 128 * U32 * y.abs() + lost_value(pre))
     if mul is not None:
         y = y * mul.to(F64)
         err = err * mul.to(F64).abs() + U32 * y.abs()

@@ -5,8 +5,8 @@ were, values that must not leak between experts."""
 import pytest
 import torch
 
-from tests.moe16_reference import (F64, U32, act, act_slope, check, half_step, linear_ref, product_bound, rounded,
-                                   spans, tiny)
+from tests.moe16_reference import (F64, U32, act, act_slope, check, linear_ref, lost_slope, lost_value,
+                                   product_bound, rounded, spans)
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.float16, torch.bfloat16]
@@ -218,14 +218,14 @@ def test_activation_gradients(dt, name, gated, counts, N, offset):
     # float32: tens of roundings of the activation (bounded like the forward
     # value); the slope's two terms are each at most 1.5 and may cancel
     wpre = d * mu * slope
-    err = 128 * U32 * (d * mu).abs() * (slope.abs() + (v * value).abs().clamp(max=1) + 1e-3) if name not in ("none", "relu") \
-        else 4 * U32 * wpre.abs()
+    err = 128 * U32 * (d * mu).abs() * (slope.abs() + (v * value).abs().clamp(max=1) + 1e-3) \
+        + lost_slope(v) * (d * mu).abs() if name not in ("none", "relu") else 4 * U32 * wpre.abs()
     for bias in (False, True):
         dpre, dmul, dbias = m.moe_linear_act_grad(dy, pre, name, mul=mul, offsets=dev, bias_grad=bias)
         check("dpre", dpre[s], wpre[s], err[s] + rounded(wpre[s], dt))
         if gated:
             wm = d * value
-            check("dmul", dmul[s], wm[s], 130 * U32 * wm[s].abs() + rounded(wm[s], dt))
+            check("dmul", dmul[s], wm[s], 130 * U32 * wm[s].abs() + rounded(wm[s], dt) + (lost_value(v) * d.abs())[s])
         else:
             assert dmul is None
         if bias:
@@ -249,12 +249,12 @@ def test_activation_tails():
         y = m.moe_linear(x, eye, activation=name, out_dtype=torch.float32)
         want = torch.nan_to_num(act(name, v.clamp(min=-1e3)))
         check(name, torch.where(v > 1e30, torch.zeros_like(y), y), torch.where(v > 1e30, torch.zeros_like(want), want),
-              160 * U32 * want.abs() + 1e-37)
+              160 * U32 * want.abs() + lost_value(v.clamp(-1e3, 1e3)) + 1e-45)
         assert float(y[0, 14]) > 2.9e38
         g = torch.ones_like(x)
         dpre, _, _ = m.moe_linear_act_grad(g, x, name)
         slope = act_slope(name, v.clamp(-1e3, 1e3))
-        check(name + " slope", dpre, slope, rounded(slope, torch.bfloat16) + 128 * U32)
+        check(name + " slope", dpre, slope, rounded(slope, torch.bfloat16) + 128 * U32 + lost_slope(v.clamp(-1e3, 1e3)))
         inf = torch.tensor([[float("inf"), float("-inf"), float("nan")]], dtype=torch.bfloat16, device="cuda")
         d, _, _ = m.moe_linear_act_grad(torch.ones_like(inf), inf, name)
         assert float(d[0, 0]) == 1.0 and float(d[0, 1]) == 0.0 and torch.isnan(d[0, 2])
