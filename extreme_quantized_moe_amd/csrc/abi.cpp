@@ -125,7 +125,7 @@ static int32_t validate_gemm(const milo_gemm_desc* d) {
 // Compute units of the current device (cached per device; 256, the MI355X
 // count, if the runtime cannot tell, e.g. on a host without a GPU where only
 // workspace sizes are queried).
-static int device_cu_count() {
+int device_cu_count() {
   static int cached[64] = {0};
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {

@@ -16,6 +16,8 @@
 //   i); f gives the rows of one read different banks.
 #pragma once
 
+#include <type_traits>
+
 #include "linear.hpp"
 
 namespace milo {
@@ -162,203 +164,295 @@ __device__ __forceinline__ void arrived() {
   __syncthreads();
 }
 
-// One tile: rows m0 .. of the expert's span (or output rows of dw), columns
-// n0 .., this split's share of the contraction.
-template <class T, int MODE, int BM, int BN, int WM, int WN>
-__device__ __forceinline__ void tile_body(const LinearArgs& a, const TileSlot& s, int m0, int n0, int split,
-                                          char* lds) {
+// First row tile, first row and row count of every expert, in LDS.
+struct ExpertTable {
+  int first[257], base[256], rows[256];
+};
+
+// One output tile's work: steps [first, last) of its contraction.
+struct Tile {
+  int e;               // -1: none left
+  int base, M, D;      // span's first row; rows (columns for dw) of the output here; contraction length
+  int m0, n0, split;
+  int first, last;
+};
+
+// Tile `id` of this launch.  All values are wave-uniform scalars.
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const ExpertTable& tab, int id) {
+  const int cols = MODE == kFwd ? a.N : a.K, tn = (cols + BN - 1) / BN;
+  const int tmw = (a.N + BM - 1) / BM;                       // dw: row tiles of every expert
+  const int per = (MODE == kDw ? a.E * tmw : __builtin_amdgcn_readfirstlane(tab.first[a.E])) * tn;
+  Tile t;
+  t.e = -1;
+  int at = xcd_order(id, per * a.splits);
+  if (at < 0) return t;
+  t.split = at / per;
+  at -= t.split * per;
+  int tm, local;
+  if (MODE == kDw) {
+    tm = tmw;
+    t.e = at / (tm * tn);
+    local = at - t.e * tm * tn;
+  } else {
+    const int q = at / tn, lane = threadIdx.x & 63;
+    int e = -1;                                              // the last expert that starts at or before row tile q
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (64 * c >= a.E) break;
+      e += __builtin_popcountll(__ballot(64 * c + lane < a.E && tab.first[64 * c + lane] <= q));
+    }
+    t.e = e;
+    const int f = __builtin_amdgcn_readfirstlane(tab.first[e]);
+    tm = __builtin_amdgcn_readfirstlane(tab.first[e + 1]) - f;
+    local = at - f * tn;
+  }
+  int mt, nt;
+  band_order(local, tm, tn, &mt, &nt);
+  t.base = __builtin_amdgcn_readfirstlane(tab.base[t.e]);
+  const int rows = __builtin_amdgcn_readfirstlane(tab.rows[t.e]);
+  t.M = MODE == kDw ? a.N : rows;
+  t.D = MODE == kFwd ? a.K : MODE == kDx ? a.N : rows;
+  t.m0 = mt * BM;
+  t.n0 = nt * BN;
+  const int all = (t.D + kDepth - 1) / kDepth, each = (all + a.splits - 1) / a.splits;
+  t.first = t.split * each < all ? t.split * each : all;
+  t.last = t.first + each < all ? t.first + each : all;
+  return t;
+}
+
+__device__ __forceinline__ void swap_odd_even_rows(float& x, float& y) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, y),
+                                                   false, false);
+  const unsigned r0 = r[0], r1 = r[1];     // a bit cast of a vector's element itself reads element 0
+  x = __builtin_bit_cast(float, r0);
+  y = __builtin_bit_cast(float, r1);
+#endif
+}
+
+// Persistent blocks: block b takes tiles b, b + grid, ...  The steps of all its
+// tiles form one stream of loads that runs two steps ahead of the products,
+// across tile borders: the next tile's operands are on their way while this
+// tile's results are written.
+//
+// A step is used in two halves of 32 contraction values; the fragments of one
+// half are read from LDS while the products of the half before run.  One
+// barrier a step, between the halves: there every wave has read the last of
+// the buffer (so the stream's next step may be loaded into it) and its part of
+// the step after has arrived.
+//
+// ACT: the activation of a forward launch (MILO_ACT_NONE also stands for
+// RELU), a template so that each kernel holds one activation's code.
+template <class T, int MODE, int ACT, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
   constexpr int NW = WM * WN, NI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr bool AW = MODE == kDw, BW = MODE != kFwd;
+  extern __shared__ __align__(16) char lds[];
+  __shared__ ExpertTable tab;
   typedef Operand<AW, BM, NW> OpA;
   typedef Operand<BW, BN, NW> OpB;
   constexpr int kBuf = OpA::kBytes + OpB::kBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = MODE == kFwd ? a.N : a.K;
-  const int M = MODE == kDw ? a.N : s.span.rows;
-  const int D = MODE == kFwd ? a.K : MODE == kDx ? a.N : s.span.rows;
   const int64_t lda = MODE == kFwd ? a.K : a.N, ldb = a.K;
-  const uint16_t* pa = (const uint16_t*)a.a + (int64_t)s.span.base * lda + (AW ? (int64_t)m0 : m0 * lda);
-  const uint16_t* pb = (const uint16_t*)a.b +
-                       (MODE == kDw ? (int64_t)s.span.base * ldb : (int64_t)s.e * a.N * a.K) +
-                       (BW ? (int64_t)n0 : n0 * ldb);
-  const int lefta = M - m0 < BM && !AW ? M - m0 : AW ? M - m0 : BM;
-  const int leftb = BW ? cols - n0 : cols - n0 < BN ? cols - n0 : BN;
 
+  if (wave == 0) {
+    int before = 0;
+    for (int c = 0; c < a.E; c += 64) {
+      const int e = c + lane;
+      const Span p = e < a.E ? expert_span(a.offsets, e, a.rows) : Span{0, 0};
+      const int n = (p.rows + BM - 1) / BM;
+      int v = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+      }
+      if (e < a.E) {
+        tab.first[e] = before + v - n;
+        tab.base[e] = p.base;
+        tab.rows[e] = p.rows;
+      }
+      before += __shfl(v, 63);
+    }
+    if (lane == 0) tab.first[a.E] = before;
+  }
+  __syncthreads();
+
+  // ---- the stream of loads
   OpA oa;
   OpB ob;
-  oa.init(lane, wave, (int)lda, M - m0);
-  ob.init(lane, wave, (int)ldb, cols - n0);
-  const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
-  Fragments<AW, BM, NI> fa;
-  Fragments<BW, BN, NJ> fb;
-  fa.init(lane, wm);
-  fb.init(lane, wn);
-  f32x4 acc[NI][NJ];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // This split's steps.  Step k is used in two halves of 32 contraction
-  // values; the fragments of one half are read from LDS while the products of
-  // the half before run.  One barrier a step, between the halves: there every
-  // wave has read the last of buffer k (so step k + 2 may be loaded into it,
-  // a whole step of products ahead of its use) and its part of step k + 1 has
-  // arrived.
-  const int all = (D + kDepth - 1) / kDepth, each = (all + a.splits - 1) / a.splits;
-  const int first = split * each, last = first + each < all ? first + each : all;
-  auto issue = [&](int k, int buf) {
+  Tile ahead;
+  int ahead_id = blockIdx.x, step = 0;
+  const uint16_t *pa = nullptr, *pb = nullptr;
+  int lefta = 0, leftb = 0;
+  auto seek = [&]() {                        // to the first tile at or after ahead_id with steps
+    for (;; ahead_id += gridDim.x) {
+      ahead = find_tile<MODE, BM, BN>(a, tab, ahead_id);
+      if (ahead.e < 0) {
+        step = 0;
+        ahead.D = ahead.last = 0;
+        return;
+      }
+      if (ahead.first < ahead.last) break;
+    }
+    step = ahead.first;
+    pa = (const uint16_t*)a.a + (int64_t)ahead.base * lda + (AW ? (int64_t)ahead.m0 : ahead.m0 * lda);
+    pb = (const uint16_t*)a.b + (MODE == kDw ? (int64_t)ahead.base * ldb : (int64_t)ahead.e * a.N * a.K) +
+         (BW ? (int64_t)ahead.n0 : ahead.n0 * ldb);
+    lefta = AW || ahead.M - ahead.m0 < BM ? ahead.M - ahead.m0 : BM;
+    leftb = BW || cols - ahead.n0 < BN ? cols - ahead.n0 : BN;
+    oa.init(lane, wave, (int)lda, ahead.M - ahead.m0);
+    ob.init(lane, wave, (int)ldb, cols - ahead.n0);
+  };
+  auto issue = [&](int buf) {
     char* dst = lds + buf * kBuf;
-    oa.load(pa, lda, lefta, D, k * kDepth, k < last, dst, wave);
-    ob.load(pb, ldb, leftb, D, k * kDepth, k < last, dst + OpA::kBytes, wave);
+    const bool on = step < ahead.last;
+    oa.load(pa, lda, lefta, ahead.D, step * kDepth, on, dst, wave);
+    ob.load(pb, ldb, leftb, ahead.D, step * kDepth, on, dst + OpA::kBytes, wave);
   };
-  s16x8 xa[2][NI], xb[2][NJ];
-  auto read = [&](int buf, int h) {
-    const char* la = lds + buf * kBuf;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) xb[h][j] = fb.read(la + OpA::kBytes, h, j);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) xa[h][i] = fa.read(la, h, i);
-  };
-  auto products = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = T::mfma(xb[h][j], xa[h][i], acc[i][j]);
-  };
-  constexpr int kReads = NI * (AW ? 2 : 1) + NJ * (BW ? 2 : 1), kLoads = OpA::kLoads + OpB::kLoads;
-  if (first < last) {
-    issue(first, 0);
-    issue(first + 1, 1);
-    arrived();
-    read(0, 0);
-    int buf = 0;
-    for (int k = first; k < last; ++k, buf ^= 1) {
-      read(buf, 1);
-      products(0);
-      interleave<NI * NJ, kReads, 0>();
-      arrived();
-      issue(k + 2, buf);
-      read(buf ^ 1, 0);          // past the last step: stale data, never used
-      products(1);
-      interleave<NI * NJ, kReads, kLoads>();
+  auto advance = [&]() {
+    if (++step >= ahead.last && ahead.e >= 0) {
+      ahead_id += gridDim.x;
+      seek();
     }
-    arrived();             // the epilogue reuses the LDS
-  }
+  };
+  oa.init(lane, wave, (int)lda, 0);
+  ob.init(lane, wave, (int)ldb, 0);
+  ahead.e = -1;
+  seek();
+  issue(0);
+  advance();
+  issue(1);
+  advance();
+  arrived();
 
-  // Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each 16 x 16 product.
-  // Each wave turns 64 x 64 results at a time around in its own 16 KB of LDS
-  // (16-byte piece c of row r at place c ^ (r mod 16)), so that a lane gets 8
-  // consecutive columns: 128-byte rows of 16-byte accesses.
-  static_assert(NJ % 4 == 0 && NI % 4 == 0, "the epilogue takes 64 x 64 results at a time");
-  char* mine = lds + wave * 16384;
+  // ---- one tile with NIX of the NI row groups of a wave
+  const int wn = wave % WN * (BN / WN);
+  Fragments<BW, BN, NJ> fb;
+  fb.init(lane, wn);
+  int buf = 0;
+  auto tile = [&](const Tile& t, auto nix) {
+    constexpr int NIX = decltype(nix)::value;
+    const int wm = wave / WN * (NIX * 16);
+    Fragments<AW, BM, NIX> fa;
+    fa.init(lane, wm);
+    f32x4 acc[NIX][NJ];
 #pragma unroll
-  for (int qq = 0; qq < NI / 4 * (NJ / 4); ++qq) {
-    const int q = qq / (NJ / 4), g = qq % (NJ / 4);
+    for (int i = 0; i < NIX; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s16x8 xa[2][NIX], xb[2][NJ];
+    auto read = [&](int b, int h) {
+      const char* la = lds + b * kBuf;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = lane & 15;
-        *(f32x4*)(mine + (16 * i + r) * 256 + (((4 * j + (lane >> 4)) ^ r) << 4)) = acc[4 * q + i][4 * g + j];
+      for (int j = 0; j < NJ; ++j) xb[h][j] = fb.read(la + OpA::kBytes, h, j);
+#pragma unroll
+      for (int i = 0; i < NIX; ++i) xa[h][i] = fa.read(la, h, i);
+    };
+    auto products = [&](int h) {
+#pragma unroll
+      for (int i = 0; i < NIX; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = T::mfma(xb[h][j], xa[h][i], acc[i][j]);
+    };
+    constexpr int kReads = NIX * (AW ? 2 : 1) + NJ * (BW ? 2 : 1), kLoads = OpA::kLoads + OpB::kLoads;
+    if (t.first < t.last) {
+      read(buf, 0);
+      for (int k = t.first; k < t.last; ++k, buf ^= 1) {
+        read(buf, 1);
+        products(0);
+        interleave<NIX * NJ, kReads, 0>();
+        arrived();
+        issue(buf);
+        read(buf ^ 1, 0);          // past the tile's last step: another's data, not used
+        products(1);
+        interleave<NIX * NJ, kReads, kLoads>();
+        advance();
       }
-    const int n = n0 + wn + 64 * g + 8 * (lane & 7), mq = m0 + wm + 64 * q + (lane >> 3);
-    const int64_t row = (MODE == kDw ? 0 : s.span.base) + (int64_t)mq;
-    // step it of a pass: row mq + 8 it, its two 16-byte pieces
-    auto lo_at = [&](int it) {
-      const int r = 8 * it + (lane >> 3);
-      return (f32x4*)(mine + r * 256 + (((2 * (lane & 7)) ^ (r & 15)) << 4));
-    };
-    auto hi_at = [&](int it) {
-      const int r = 8 * it + (lane >> 3);
-      return (f32x4*)(mine + r * 256 + (((2 * (lane & 7) + 1) ^ (r & 15)) << 4));
-    };
-    if (a.splits > 1) {
-      const int64_t rows = MODE == kDw ? (int64_t)a.E * a.N : a.rows;
-      float* part = a.part + (split * rows + (MODE == kDw ? (int64_t)s.e * a.N : 0) + row) * cols + n;
-#pragma unroll
-      for (int it = 0; it < 8; ++it)
-        if (mq + 8 * it < M && n < cols) {
-          *(f32x4*)(part + (int64_t)8 * it * cols) = *lo_at(it);
-          *(f32x4*)(part + (int64_t)8 * it * cols + 4) = *hi_at(it);
-        }
-      continue;
     }
-    // What the epilogue reads is asked for before the first pass: its latency
-    // is paid once for the 64 x 64 results, not once a row.
+
+    // ---- results.  Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each
+    // 16 x 16 product; exchanging rows of lanes between two neighbouring
+    // products gives it 8 consecutive columns of the 32: 16-byte accesses.
+    // What the epilogue reads is asked for two row groups at a time.
+    const int n = t.n0 + wn + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+    const int64_t row0 = (MODE == kDw ? (int64_t)t.e * a.N : t.base) + (int64_t)t.m0 + wm + (lane & 15);
+    const int rows_left = t.M - t.m0 - wm - (lane & 15);
     const bool has_mul = MODE == kFwd && a.mul, has_add = MODE != kDw && a.residual;
-    Pack<T, 8> bias = {}, mul[8], add[8];
-    if (MODE == kFwd && a.bias && n < cols) bias = load_pack<T, 8>(a.bias, (int64_t)s.e * a.N + n);
-    if (has_mul) {
+    Pack<T, 8> bias[NJ / 2] = {};
+    if (MODE == kFwd && a.bias && a.splits == 1) {
 #pragma unroll
-      for (int it = 0; it < 8; ++it)
-        if (mq + 8 * it < M && n < cols) mul[it] = load_pack<T, 8>(a.mul, (row + 8 * it) * cols + n);
+      for (int j = 0; j < NJ / 2; ++j)
+        if (n + 32 * j < cols) bias[j] = load_pack<T, 8>(a.bias, (int64_t)t.e * a.N + n + 32 * j);
     }
-    if (has_add) {
 #pragma unroll
-      for (int it = 0; it < 8; ++it)
-        if (mq + 8 * it < M && n < cols) add[it] = load_pack<T, 8>(a.residual, (row + 8 * it) * cols + n);
-    }
-    if (MODE == kFwd && (a.bias || a.pre || a.act != MILO_ACT_NONE)) {
-      // bias, kept pre-activation and activation, back into LDS: one copy of
-      // the activations' code
-#pragma unroll 1
-      for (int it = 0; it < 8; ++it) {
-        if (mq + 8 * it >= M || n >= cols) continue;
-        const f32x4 lo = *lo_at(it), hi = *hi_at(it);
-        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if (a.bias) add_pack<T, 8>(v, bias);
-        if (a.pre) store_pack<T, 8>(a.pre, (row + 8 * it) * cols + n, v);
-        if (a.act != MILO_ACT_NONE) {
+    for (int q = 0; q < NIX / 2; ++q) {
+      Pack<T, 8> mul[2][NJ / 2], add[2][NJ / 2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = act_value(a.act, v[i]);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          const int r = 32 * q + 16 * i;
+          if (r >= rows_left || n + 32 * j >= cols || a.splits > 1) continue;
+          if (has_mul) mul[i][j] = load_pack<T, 8>(a.mul, (row0 + r) * cols + n + 32 * j);
+          if (has_add) add[i][j] = load_pack<T, 8>(a.residual, (row0 + r) * cols + n + 32 * j);
         }
-        *lo_at(it) = f32x4{v[0], v[1], v[2], v[3]};
-        *hi_at(it) = f32x4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          f32x4 lo = acc[2 * q + i][2 * j], hi = acc[2 * q + i][2 * j + 1];
+          float v[8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v[c] = lo[c];
+            v[4 + c] = hi[c];
+            swap_odd_even_rows(v[c], v[4 + c]);
+          }
+          const int r = 32 * q + 16 * i;
+          if (r >= rows_left || n + 32 * j >= cols) continue;
+          const int64_t at = (row0 + r) * cols + n + 32 * j;
+          if (a.splits > 1) {
+            float* part = a.part + (int64_t)t.split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols + at;
+            *(f32x4*)part = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4*)(part + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            continue;
+          }
+          if constexpr (MODE == kFwd) {
+            if (a.bias) add_pack<T, 8>(v, bias[j]);
+            if (a.pre) store_pack<T, 8>(a.pre, at, v);
+            if (ACT != MILO_ACT_NONE) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) v[c] = act_value(ACT, v[c]);
+            } else if (a.act == MILO_ACT_RELU) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) v[c] = act_value(MILO_ACT_RELU, v[c]);
+            }
+            if (has_mul) mul_pack<T, 8>(v, mul[i][j]);
+          }
+          if (has_add) add_pack<T, 8>(v, add[i][j]);
+          store_out<T, 8>(a, at, v);
+        }
+    }
+  };
+
+  // A tile with at most half of its rows runs at half the height: a good part
+  // of the experts' last row tiles would otherwise multiply mostly nothing.
+  for (int id = blockIdx.x;; id += gridDim.x) {
+    const Tile t = find_tile<MODE, BM, BN>(a, tab, id);
+    if (t.e < 0) break;
+    if constexpr (NI == 8) {
+      if (t.M - t.m0 <= BM / 2) {
+        tile(t, std::integral_constant<int, NI / 2>());
+        continue;
       }
     }
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      if (mq + 8 * it >= M || n >= cols) continue;
-      const f32x4 lo = *lo_at(it), hi = *hi_at(it);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (has_mul) mul_pack<T, 8>(v, mul[it]);
-      if (has_add) add_pack<T, 8>(v, add[it]);
-      store_out<T, 8>(a, out_at<MODE>(a, s.e, row + 8 * it, n), v);
-    }
+    tile(t, std::integral_constant<int, NI>());
   }
-}
-
-// A row tile with at most half of its rows runs a form of half the height (a
-// quarter of the experts' last tiles otherwise multiply mostly nothing).
-template <class T, int MODE, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
-  extern __shared__ __align__(16) char lds[];
-  static_assert(tile_lds<BM, BN>() >= (size_t)WM * WN * 16384, "the epilogue's staging fits");
-  const int tn = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
-  TileSlot s;
-  int mt, nt;
-  if constexpr (MODE == kDw) {
-    const int tm = (a.N + BM - 1) / BM, id = xcd_order(blockIdx.x, a.E * tm * tn);
-    if (id < 0) return;
-    s.e = id / (tm * tn);
-    s.span = expert_span(a.offsets, s.e, a.rows);
-    band_order(id - s.e * tm * tn, tm, tn, &mt, &nt);
-  } else {
-    const int id = blockIdx.x;
-    s = find_slot(a.offsets, a.E, a.rows, BM, tn, [&](int total) { return xcd_order(id, total); });
-    if (s.e < 0) return;
-    band_order(s.local, s.row_tiles, tn, &mt, &nt);
-  }
-  const int m0 = mt * BM, left = (MODE == kDw ? a.N : s.span.rows) - m0;
-  if constexpr (BM == 256) {
-    if (left <= BM / 2) {
-      tile_body<T, MODE, BM / 2, BN, WM, WN>(a, s, m0, nt * BN, blockIdx.y, lds);
-      return;
-    }
-  }
-  tile_body<T, MODE, BM, BN, WM, WN>(a, s, m0, nt * BN, blockIdx.y, lds);
 #endif
 }
 

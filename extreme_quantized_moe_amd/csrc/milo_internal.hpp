@@ -217,6 +217,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ offset
 // ---------------------------------------------------------------- host side
 void set_error(const char* fmt, ...);
 int32_t hip_status(hipError_t e, const char* what);
+int device_cu_count();   // compute units of the current device
 
 // launchers (return MILO_OK or MILO_ERR_HIP)
 int32_t launch_quantize(const float* W, int64_t rows, int64_t K, int group, uint8_t* codes,
