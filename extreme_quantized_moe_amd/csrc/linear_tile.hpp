@@ -84,6 +84,18 @@ struct Operand {
   }
 };
 
+// A transposing LDS read.  `restrict` tells the compiler that no load into LDS
+// in flight writes what is read (the barriers see to that); without it every
+// such read waits for all of them.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 read_transposed(const lds_s16x4* __restrict__ p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+#else
+  return s16x4{};
+#endif
+}
+
 // Fragments of NF 16-wide groups starting at row (column) w0 of an LDS tile.
 template <bool WIDE, int ROWS, int NF>
 struct Fragments {
@@ -105,10 +117,8 @@ struct Fragments {
     if constexpr (!WIDE) {
       return *(const s16x8*)(lds + off[s] + t * 16 * kDepth * 2);
     } else {
-      typedef __attribute__((address_space(3))) s16x4 lds4;
       const char* p = lds + off[t] + s * 32 * ROWS * 2;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * ROWS * 2));
+      const s16x4 lo = read_transposed((const lds_s16x4*)p), hi = read_transposed((const lds_s16x4*)(p + 4 * ROWS * 2));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
