@@ -284,19 +284,22 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, 
 }
 
 // ---------------------------------------------------------------- host side
+constexpr int kLinearStep = 64;   // contraction values per step of the tile kernels
+
 // How one product is run (host side; chosen from sizes, types and alignment).
 struct LinearPlan {
   int kernel;          // kPlan*
   int splits;
   size_t part_bytes;   // fp32 partial sums of a split contraction
 };
-enum { kPlanGeneral = 0, kPlanFew, kPlanTile128, kPlanTile256 };
+enum { kPlanGeneral = 0, kPlanFew, kPlanNarrow, kPlanTile128, kPlanTile256 };
 
 LinearPlan plan_linear(int mode, const LinearArgs& a);
 int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
 int32_t launch_linear_general(int mode, int dtype, const LinearArgs& a, hipStream_t st);
 int32_t launch_linear_tile(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st);
-int32_t launch_linear_few(int dtype, const LinearArgs& a, hipStream_t st);
+int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, hipStream_t st);
+int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, hipStream_t st);
 size_t act_grad_workspace_bytes(int E, int N, int rows);
 int32_t launch_act_grad(const void* dy, const void* pre, const void* mul, const int32_t* offsets, int E, int N,
                         int rows, int dtype, int act, void* dpre, void* dmul, float* dbias, float* part,

@@ -101,6 +101,20 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 #endif
 }
 
+// The same walk for few columns and many rows (a router): a block takes 16
+// rows and 64 columns, so it is x that is streamed once and w that every
+// block reads again, from the L2.
+template <class T>
+__global__ void __launch_bounds__(512) linear_narrow_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(16) float lds[8 * 16 * (64 + 4)];
+  const int id = blockIdx.x, width = (a.N + 63) / 64;
+  const TileSlot s = find_slot(a.offsets, a.E, a.rows, 16, width, [&](int) { return id; });
+  if (s.e < 0) return;
+  few_rows<T, 1, 4, 8>(a, s.e, s.span.base, s.local / width * 16, s.span.rows, s.local % width * 64, lds);
+#endif
+}
+
 template <class T>
 static void run_few(const LinearArgs& a, hipStream_t st) {
   // two column groups a block halve the traffic of x; with few columns in all
@@ -116,9 +130,15 @@ static void run_few(const LinearArgs& a, hipStream_t st) {
 #undef RUN
 }
 
-int32_t launch_linear_few(int dtype, const LinearArgs& a, hipStream_t st) {
-  if (dtype == MILO_F16) run_few<F16>(a, st);
-  else run_few<BF16>(a, st);
+template <class T>
+static void run_narrow(const LinearArgs& a, hipStream_t st) {
+  const int64_t blocks = ((int64_t)(a.rows + 15) / 16 + (a.E > 1 ? a.E : 0)) * ((a.N + 63) / 64);
+  hipLaunchKernelGGL(linear_narrow_kernel<T>, dim3((unsigned)blocks), dim3(512), 0, st, a);
+}
+
+int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, hipStream_t st) {
+  if (dtype == MILO_F16) { if (narrow) run_narrow<F16>(a, st); else run_few<F16>(a, st); }
+  else { if (narrow) run_narrow<BF16>(a, st); else run_few<BF16>(a, st); }
   return hip_status(hipGetLastError(), "linear_few_kernel launch");
 }
 

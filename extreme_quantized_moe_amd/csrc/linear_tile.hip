@@ -8,8 +8,8 @@ static hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
   const int64_t tn = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
   const int64_t rows = MODE == kDw ? (int64_t)a.E * ((a.N + BM - 1) / BM)
                                    : (a.rows + BM - 1) / BM + (a.E > 1 ? a.E : 0);
-  // as many blocks as run at once (one or two to a compute unit), a multiple
-  // of 8 so that a block's tiles stay on its XCD
+  // as many blocks as run at once (one or two to a compute unit: the LDS
+  // ring), a multiple of 8 so that a block's tiles stay on its XCD
   const int64_t slots = (int64_t)device_cu_count() * (BM == 256 ? 1 : 2);
   int64_t blocks = rows * tn * a.splits;
   blocks = (blocks < slots ? blocks + 7 : slots) / 8 * 8;
@@ -41,6 +41,58 @@ static hipError_t run_type(int mode, const LinearArgs& a, int kernel, hipStream_
     case MILO_ACT_GELU_TANH: return run_mode<T, kFwd, MILO_ACT_GELU_TANH>(a, kernel, st);
     default: return run_mode<T, kFwd, MILO_ACT_NONE>(a, kernel, st);
   }
+}
+
+// ---- split contraction: the partial sums of each result in split order, then
+// the epilogue.  A wave takes one row, a lane 8 columns.
+template <class T, int MODE>
+__global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a) {
+  const int cols = MODE == kFwd ? a.N : a.K;
+  const int n = (blockIdx.y * 64 + (threadIdx.x & 63)) * 8, wave = threadIdx.x >> 6;
+  int e;
+  int64_t row;
+  if (MODE == kDw) {
+    const int64_t r = (int64_t)blockIdx.x * 4 + wave;
+    e = (int)(r / a.N);
+    row = r - (int64_t)e * a.N;
+    if (e >= a.E) return;
+  } else {
+    const int id = blockIdx.x;
+    const TileSlot s = find_slot(a.offsets, a.E, a.rows, 4, 1, [&](int) { return id; });
+    if (s.e < 0 || s.local * 4 + wave >= s.span.rows) return;
+    e = s.e;
+    row = s.span.base + (int64_t)s.local * 4 + wave;
+  }
+  if (n >= cols) return;
+  const int64_t one = (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols, at = out_at<MODE>(a, e, row, n);
+  f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+  for (int s = 0; s < a.splits; ++s) {
+    lo += *(const f32x4*)(a.part + s * one + at);
+    hi += *(const f32x4*)(a.part + s * one + at + 4);
+  }
+  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  finish<T, MODE, 8>(a, e, row, n, v);
+}
+
+template <class T, int MODE>
+static void run_join(const LinearArgs& a, hipStream_t st) {
+  const int cols = MODE == kFwd ? a.N : a.K;
+  const int64_t quads = MODE == kDw ? ((int64_t)a.E * a.N + 3) / 4 : (a.rows + 3) / 4 + (a.E > 1 ? a.E : 0);
+  hipLaunchKernelGGL((linear_join_kernel<T, MODE>), dim3((unsigned)quads, (unsigned)((cols + 511) / 512)), dim3(256),
+                     0, st, a);
+}
+
+template <class T>
+static void run_join_mode(int mode, const LinearArgs& a, hipStream_t st) {
+  if (mode == kFwd) run_join<T, kFwd>(a, st);
+  else if (mode == kDx) run_join<T, kDx>(a, st);
+  else run_join<T, kDw>(a, st);
+}
+
+int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, hipStream_t st) {
+  if (dtype == MILO_F16) run_join_mode<F16>(mode, a, st);
+  else run_join_mode<BF16>(mode, a, st);
+  return hip_status(hipGetLastError(), "linear_join_kernel launch");
 }
 
 int32_t launch_linear_tile(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st) {

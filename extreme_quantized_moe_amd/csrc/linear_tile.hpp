@@ -22,7 +22,7 @@
 
 namespace milo {
 
-constexpr int kDepth = 64;                 // contraction values per step
+constexpr int kDepth = kLinearStep;        // contraction values per step
 constexpr int kTileRsrcWord3 = 0x00020000; // raw buffer, bounds checked in bytes
 constexpr int kOutside = 0x7FFFFFF0;       // an offset no operand reaches
 

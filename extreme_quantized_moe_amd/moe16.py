@@ -23,14 +23,15 @@ def _need(ok, what):
 
 def _tensor(name, t, dtype, shape, dev=None):
     """Refuses a tensor the kernels could not address as they will."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and (dev is None or t.device == dev):
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: libmilo needs contiguous CUDA (HIP) tensors")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the first operand on {dev}")
+    raise ValueError(f"{name} is on {t.device}, the first operand on {dev}")
 
 
 def _float_type(name, t, wide=True):
@@ -45,13 +46,19 @@ def _ptr(t):
 
 
 def _run(name, dev, *args):
-    """Calls milo_<name>(*args, stream) with the tensors' device current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        check(name, getattr(L.lib(), name)(*args, stream))
+    """Calls milo_<name>(*args, stream) on the device's current stream, with
+    the device current.  (torch.cuda.current_stream builds a Stream object for
+    this; a decoding step's calls take a few microseconds in all.)"""
+    index = dev.index
+    fn = getattr(L.lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            check(name, getattr(L.lib(), name)(*args, stream))
+            rc = fn(*args, stream)
+    if rc:
+        check(name, rc)
 
 
 def _scratch(nbytes, dev):
@@ -208,30 +215,22 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
     _tensor("x", x, dt, (R, K))
     _tensor("w", w, dt, w.shape, dev)
     _offsets(offsets, E, dev)
-    d = L.MiloLinearDesc()
     if bias is not None:
         _tensor("bias", bias, dt, (N,) if bias.dim() == 1 and E == 1 else (E, N), dev)
-        d.bias = bias.data_ptr()
     if mul is not None:
         _tensor("mul", mul, dt, (R, N), dev)
-        d.mul = mul.data_ptr()
     if residual is not None:
         _tensor("residual", residual, dt, (R, N), dev)
-        d.residual = residual.data_ptr()
     odt = dt if out_dtype is None else out_dtype
     _need(odt in (dt, torch.float32), f"out_dtype must be {dt} or torch.float32")
     if out is None:
         out = torch.empty((R, N), dtype=odt, device=dev)
     else:
         _tensor("out", out, odt, (R, N), dev)
-    pre = None
-    if return_pre:
-        pre = torch.empty((R, N), dtype=dt, device=dev)
-        d.pre = pre.data_ptr()
-    d.num_experts, d.N, d.K, d.num_rows, d.max_rows_per_expert = E, N, K, R, max_rows_per_expert
-    d.dtype, d.out_dtype, d.activation = code, L.F32 if odt == torch.float32 else code, _act(activation)
-    d.x, d.w, d.offsets, d.y = x.data_ptr(), w.data_ptr(), _ptr(offsets), out.data_ptr()
-    ref = C.byref(d)
+    pre = torch.empty((R, N), dtype=dt, device=dev) if return_pre else None
+    ref = C.byref(L.MiloLinearDesc(
+        E, N, K, R, max_rows_per_expert, code, L.F32 if odt is torch.float32 else code, _act(activation), x.data_ptr(),
+        w.data_ptr(), _ptr(offsets), _ptr(bias), _ptr(mul), _ptr(residual), _ptr(pre), out.data_ptr()))
     nbytes = L.lib().milo_moe_linear_workspace_bytes(ref)
     ws = _scratch(nbytes, dev)
     _run("milo_moe_linear", dev, ref, _ptr(ws), nbytes)
@@ -277,7 +276,6 @@ def moe_linear_grad(dy, x, w, offsets=None, need_dx=True, need_dw=True, dw_dtype
     _tensor("x", x, dt, (R, K), dev)
     _tensor("w", w, dt, w.shape, dev)
     _offsets(offsets, E, dev)
-    d = L.MiloLinearGradDesc()
     odt = dt if dw_dtype is None else dw_dtype
     _need(odt in (dt, torch.float32), f"dw_dtype must be {dt} or torch.float32")
     dx = torch.empty((R, K), dtype=dt, device=dev) if need_dx else None
@@ -285,12 +283,9 @@ def moe_linear_grad(dy, x, w, offsets=None, need_dx=True, need_dw=True, dw_dtype
     if dx_add is not None:
         _need(need_dx, "dx_add without dx")
         _tensor("dx_add", dx_add, dt, (R, K), dev)
-        d.dx_add = dx_add.data_ptr()
-    d.num_experts, d.N, d.K, d.num_rows = E, N, K, R
-    d.dtype, d.dw_dtype = code, L.F32 if odt == torch.float32 else code
-    d.dy, d.x, d.w, d.offsets = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(offsets)
-    d.dx, d.dw = _ptr(dx), _ptr(dw)
-    ref = C.byref(d)
+    ref = C.byref(L.MiloLinearGradDesc(
+        E, N, K, R, code, L.F32 if odt is torch.float32 else code, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
+        _ptr(offsets), _ptr(dx_add), _ptr(dx), _ptr(dw)))
     nbytes = L.lib().milo_moe_linear_grad_workspace_bytes(ref)
     ws = _scratch(nbytes, dev)
     _run("milo_moe_linear_grad", dev, ref, _ptr(ws), nbytes)
