@@ -242,6 +242,20 @@ __device__ __forceinline__ void swap_odd_even_rows(float& x, float& y) {
 #endif
 }
 
+template <class T>
+using Packed8 = Pack<T, 8>;
+
+// 8 values rounded to the 16-bit type.
+template <class T>
+__device__ __forceinline__ u32x4 rounded(const float* v) {
+  Pack<T, 8> o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o.v[i] = T::down(v[i]);
+  return __builtin_bit_cast(u32x4, o);
+}
+
+constexpr int kAhead = 2;   // row groups whose epilogue operands are asked for at a time
+
 // Persistent blocks: block b takes tiles b, b + grid, ...  The steps of all its
 // tiles form one stream of loads that runs two steps ahead of the products,
 // across tile borders: the next tile's operands are on their way while this
@@ -386,36 +400,70 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
     }
 
     // ---- results.  Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each
-    // 16 x 16 product; exchanging rows of lanes between two neighbouring
-    // products gives it 8 consecutive columns of the 32: 16-byte accesses.
-    // What the epilogue reads is asked for two row groups at a time.
+    // 16 x 16 product.  All accesses go through buffer resources that begin at
+    // the tile and end with its last row, columns past the end get an offset
+    // outside: no branches, so the compiler keeps many in flight.  No scalar
+    // offsets here: with one, a 16-byte store's data registers were overwritten
+    // by the next lane exchange before the store had read them (lanes 12..15
+    // of its first word); without one the compiler knows the wait it needs.
+    const int lane_row = lane & 15;
+    const int rows_here = t.M - t.m0 < BM ? t.M - t.m0 : BM;
+    const int64_t origin = ((MODE == kDw ? (int64_t)t.e * a.N : t.base) + (int64_t)t.m0) * cols;
+    auto rsrc = [&](const void* p, int bytes) __attribute__((always_inline)) {
+      return __builtin_amdgcn_make_buffer_rsrc((char*)p + origin * bytes, 0, rows_here * cols * bytes, kTileRsrcWord3);
+    };
+    if (a.splits > 1 || (MODE == kDw && a.out_f32)) {
+      // float32 as it is: 64 contiguous bytes a row
+      float* dst = (float*)a.out;
+      if (a.splits > 1) dst = a.part + (int64_t)t.split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols;
+      const __amdgpu_buffer_rsrc_t r = rsrc(dst, 4);
+      const int n = t.n0 + wn + 4 * (lane >> 4), at = ((wm + lane_row) * cols + n) * 4;
+#pragma unroll
+      for (int i = 0; i < NIX; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), r,
+                                                 (n + 16 * j < cols ? at + 64 * j : kOutside) + 64 * i * cols, 0, 0);
+      return;
+    }
+    // Exchanging rows of lanes between two neighbouring products gives a lane
+    // 8 consecutive columns of the 32.
     const int n = t.n0 + wn + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
-    const int64_t row0 = (MODE == kDw ? (int64_t)t.e * a.N : t.base) + (int64_t)t.m0 + wm + (lane & 15);
-    const int rows_left = t.M - t.m0 - wm - (lane & 15);
+    const int at = (wm + lane_row) * cols + n;
     const bool has_mul = MODE == kFwd && a.mul, has_add = MODE != kDw && a.residual;
     Pack<T, 8> bias[NJ / 2] = {};
-    if (MODE == kFwd && a.bias && a.splits == 1) {
+    if (MODE == kFwd && a.bias) {
 #pragma unroll
       for (int j = 0; j < NJ / 2; ++j)
         if (n + 32 * j < cols) bias[j] = load_pack<T, 8>(a.bias, (int64_t)t.e * a.N + n + 32 * j);
     }
+    const __amdgpu_buffer_rsrc_t rm = rsrc(has_mul ? a.mul : a.out, 2), ra = rsrc(has_add ? a.residual : a.out, 2),
+                                 rp = rsrc(MODE == kFwd && a.pre ? a.pre : a.out, 2), ro = rsrc(a.out, a.out_f32 ? 4 : 2);
 #pragma unroll
-    for (int q = 0; q < NIX / 2; ++q) {
-      Pack<T, 8> mul[2][NJ / 2], add[2][NJ / 2];
+    for (int q = 0; q < NIX / kAhead; ++q) {
+      u32x4 mul[kAhead][NJ / 2], add[kAhead][NJ / 2];
+      if (has_mul) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ / 2; ++j)
+            mul[i][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                rm, (n + 32 * j < cols ? 2 * at + 64 * j : kOutside) + 32 * (kAhead * q + i) * cols, 0, 0);
+      }
+      if (has_add) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ / 2; ++j)
+            add[i][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                ra, (n + 32 * j < cols ? 2 * at + 64 * j : kOutside) + 32 * (kAhead * q + i) * cols, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
 #pragma unroll
         for (int j = 0; j < NJ / 2; ++j) {
-          const int r = 32 * q + 16 * i;
-          if (r >= rows_left || n + 32 * j >= cols || a.splits > 1) continue;
-          if (has_mul) mul[i][j] = load_pack<T, 8>(a.mul, (row0 + r) * cols + n + 32 * j);
-          if (has_add) add[i][j] = load_pack<T, 8>(a.residual, (row0 + r) * cols + n + 32 * j);
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ / 2; ++j) {
-          f32x4 lo = acc[2 * q + i][2 * j], hi = acc[2 * q + i][2 * j + 1];
+          const int g = kAhead * q + i;
+          const f32x4 lo = acc[g][2 * j], hi = acc[g][2 * j + 1];
           float v[8];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -423,18 +471,10 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
             v[4 + c] = hi[c];
             swap_odd_even_rows(v[c], v[4 + c]);
           }
-          const int r = 32 * q + 16 * i;
-          if (r >= rows_left || n + 32 * j >= cols) continue;
-          const int64_t at = (row0 + r) * cols + n + 32 * j;
-          if (a.splits > 1) {
-            float* part = a.part + (int64_t)t.split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols + at;
-            *(f32x4*)part = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4*)(part + 4) = f32x4{v[4], v[5], v[6], v[7]};
-            continue;
-          }
+          const int off = (n + 32 * j < cols ? 2 * at + 64 * j : kOutside) + 32 * g * cols;
           if constexpr (MODE == kFwd) {
             if (a.bias) add_pack<T, 8>(v, bias[j]);
-            if (a.pre) store_pack<T, 8>(a.pre, at, v);
+            if (a.pre) __builtin_amdgcn_raw_buffer_store_b128(rounded<T>(v), rp, off, 0, 0);
             if (ACT != MILO_ACT_NONE) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) v[c] = act_value(ACT, v[c]);
@@ -442,10 +482,18 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
 #pragma unroll
               for (int c = 0; c < 8; ++c) v[c] = act_value(MILO_ACT_RELU, v[c]);
             }
-            if (has_mul) mul_pack<T, 8>(v, mul[i][j]);
+            if (has_mul) mul_pack<T, 8>(v, __builtin_bit_cast(Packed8<T>, mul[i][j]));
           }
-          if (has_add) add_pack<T, 8>(v, add[i][j]);
-          store_out<T, 8>(a, at, v);
+          if (has_add) add_pack<T, 8>(v, __builtin_bit_cast(Packed8<T>, add[i][j]));
+          if (MODE != kFwd || !a.out_f32) {
+            __builtin_amdgcn_raw_buffer_store_b128(rounded<T>(v), ro, off, 0, 0);
+          } else {
+            const int wide = (n + 32 * j < cols ? 4 * at + 128 * j : kOutside) + 64 * g * cols;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), ro, wide, 0,
+                                                   0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}), ro,
+                                                   wide + 16, 0, 0);
+          }
         }
     }
   };
