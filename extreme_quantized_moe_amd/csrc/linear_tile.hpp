@@ -125,12 +125,30 @@ struct Fragments {
 };
 
 // Block -> tile.  Blocks go to the 8 XCDs in turn; each XCD gets a run of
-// consecutive tiles, so that tiles sharing operands share its L2.
-__device__ __forceinline__ int xcd_order(int id, int total) {
-  const int q = total >> 3, r = total & 7, x = id & 7, i = id >> 3;
-  if (i >= q + (x < r ? 1 : 0)) return -1;
-  return x * q + (x < r ? x : r) + i;
+// consecutive full tiles, so that tiles sharing operands share its L2, and then
+// a run of the short tiles (a row tile with at most half of its rows), which
+// fill the last round: among the full ones they unbalanced it (8192 ragged rows
+// over 8 experts x 14336 x 4096: 1033 us mixed).
+struct TileIndex {
+  int at;        // -1: none left
+  bool short_;
+};
+__device__ __forceinline__ TileIndex xcd_order(int id, int full, int shorts) {
+  const int x = id & 7;
+  int i = id >> 3;
+  const int nf = (full >> 3) + (x < (full & 7) ? 1 : 0), ns = (shorts >> 3) + (x < (shorts & 7) ? 1 : 0);
+  if (i < nf) return {x * (full >> 3) + min(x, full & 7) + i, false};
+  i -= nf;
+  if (i < ns) return {x * (shorts >> 3) + min(x, shorts & 7) + i, true};
+  return {-1, false};
 }
+
+// Row tiles of `rows` rows that have more than half of them, and whether a
+// short one follows.
+template <int BM>
+__device__ __forceinline__ int full_tiles(int rows) { return (rows + BM / 2 - 1) / BM; }
+template <int BM>
+__device__ __forceinline__ int short_tiles(int rows) { return rows > full_tiles<BM>(rows) * BM ? 1 : 0; }
 
 // Within an expert: bands of kBand column tiles, row tiles inside a band.
 constexpr int kBand = 8;
@@ -174,9 +192,9 @@ __device__ __forceinline__ void arrived() {
   __syncthreads();
 }
 
-// First row tile, first row and row count of every expert, in LDS.
+// Full and short row tiles before each expert's, its first row and row count, in LDS.
 struct ExpertTable {
-  int first[257], base[256], rows[256];
+  int first[2][257], base[256], rows[256];
 };
 
 // One output tile's work: steps [first, last) of its contraction.
@@ -191,30 +209,34 @@ struct Tile {
 template <int MODE, int BM, int BN>
 __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const ExpertTable& tab, int id) {
   const int cols = MODE == kFwd ? a.N : a.K, tn = (cols + BN - 1) / BN;
-  const int tmw = (a.N + BM - 1) / BM;                       // dw: row tiles of every expert
-  const int per = (MODE == kDw ? a.E * tmw : __builtin_amdgcn_readfirstlane(tab.first[a.E])) * tn;
+  // dw: every expert has the same row tiles
+  const int fw = full_tiles<BM>(a.N), sw = short_tiles<BM>(a.N);
+  const int full = (MODE == kDw ? a.E * fw : __builtin_amdgcn_readfirstlane(tab.first[0][a.E])) * tn;
+  const int shorts = (MODE == kDw ? a.E * sw : __builtin_amdgcn_readfirstlane(tab.first[1][a.E])) * tn;
   Tile t;
   t.e = -1;
-  int at = xcd_order(id, per * a.splits);
-  if (at < 0) return t;
-  t.split = at / per;
-  at -= t.split * per;
-  int tm, local;
+  const TileIndex x = xcd_order(id, full * a.splits, shorts * a.splits);
+  if (x.at < 0) return t;
+  const int per = x.short_ ? shorts : full;
+  t.split = x.at / per;
+  const int at = x.at - t.split * per;
+  int tm, local;       // row tiles of this kind of the expert, index among its tiles of this kind
   if (MODE == kDw) {
-    tm = tmw;
+    tm = x.short_ ? sw : fw;
     t.e = at / (tm * tn);
     local = at - t.e * tm * tn;
   } else {
+    const int* first = tab.first[x.short_ ? 1 : 0];
     const int q = at / tn, lane = threadIdx.x & 63;
     int e = -1;                                              // the last expert that starts at or before row tile q
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (64 * c >= a.E) break;
-      e += __builtin_popcountll(__ballot(64 * c + lane < a.E && tab.first[64 * c + lane] <= q));
+      e += __builtin_popcountll(__ballot(64 * c + lane < a.E && first[64 * c + lane] <= q));
     }
     t.e = e;
-    const int f = __builtin_amdgcn_readfirstlane(tab.first[e]);
-    tm = __builtin_amdgcn_readfirstlane(tab.first[e + 1]) - f;
+    const int f = __builtin_amdgcn_readfirstlane(first[e]);
+    tm = __builtin_amdgcn_readfirstlane(first[e + 1]) - f;
     local = at - f * tn;
   }
   int mt, nt;
@@ -223,7 +245,7 @@ __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const ExpertTable
   const int rows = __builtin_amdgcn_readfirstlane(tab.rows[t.e]);
   t.M = MODE == kDw ? a.N : rows;
   t.D = MODE == kFwd ? a.K : MODE == kDx ? a.N : rows;
-  t.m0 = mt * BM;
+  t.m0 = (x.short_ ? full_tiles<BM>(t.M) : mt) * BM;
   t.n0 = nt * BN;
   const int all = (t.D + kDepth - 1) / kDepth, each = (all + a.splits - 1) / a.splits;
   t.first = t.split * each < all ? t.split * each : all;
@@ -284,25 +306,31 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   const int64_t lda = MODE == kFwd ? a.K : a.N, ldb = a.K;
 
   if (wave == 0) {
-    int before = 0;
+    int before[2] = {0, 0};
     for (int c = 0; c < a.E; c += 64) {
       const int e = c + lane;
       const Span p = e < a.E ? expert_span(a.offsets, e, a.rows) : Span{0, 0};
-      const int n = (p.rows + BM - 1) / BM;
-      int v = n;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-      }
       if (e < a.E) {
-        tab.first[e] = before + v - n;
         tab.base[e] = p.base;
         tab.rows[e] = p.rows;
       }
-      before += __shfl(v, 63);
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const int n = kind ? short_tiles<BM>(p.rows) : full_tiles<BM>(p.rows);
+        int v = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int u = __shfl_up(v, d);
+          if (lane >= d) v += u;
+        }
+        if (e < a.E) tab.first[kind][e] = before[kind] + v - n;
+        before[kind] += __shfl(v, 63);
+      }
     }
-    if (lane == 0) tab.first[a.E] = before;
+    if (lane == 0) {
+      tab.first[0][a.E] = before[0];
+      tab.first[1][a.E] = before[1];
+    }
   }
   __syncthreads();
 
