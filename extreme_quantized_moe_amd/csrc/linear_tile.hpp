@@ -128,7 +128,7 @@ struct Fragments {
 // consecutive full tiles, so that tiles sharing operands share its L2, and then
 // a run of the short tiles (a row tile with at most half of its rows), which
 // fill the last round: among the full ones they unbalanced it (8192 ragged rows
-// over 8 experts x 14336 x 4096: 1033 us mixed).
+// over 8 experts x 14336 x 4096: 1033 us mixed, 985 apart).
 struct TileIndex {
   int at;        // -1: none left
   bool short_;
@@ -141,6 +141,24 @@ __device__ __forceinline__ TileIndex xcd_order(int id, int full, int shorts) {
   i -= nf;
   if (i < ns) return {x * (shorts >> 3) + min(x, shorts & 7) + i, true};
   return {-1, false};
+}
+
+// dw: an expert's tiles cost as its rows do, so every XCD gets an eighth of
+// each expert's tiles (`each` of them: experts in turn, the eighths rotating),
+// not a run over experts.  Positions past an expert's last tile are skipped.
+// Moves id to the tile it returns.
+__device__ __forceinline__ TileIndex spread_order(int& id, int stride, int E, int full, int shorts) {
+  const int ef = (full + 7) >> 3, es = (shorts + 7) >> 3;
+  for (;; id += stride) {
+    const int x = id & 7;
+    int i = id >> 3;
+    const bool s = i >= E * ef;
+    if (s) i -= E * ef;
+    const int each = s ? es : ef, all = s ? shorts : full;
+    if (i >= E * each) return {-1, false};
+    const int e = i / each, local = ((x + e) & 7) * each + i - e * each;
+    if (local < all) return {e * all + local, s};
+  }
 }
 
 // Row tiles of `rows` rows that have more than half of them, and whether a
@@ -205,27 +223,31 @@ struct Tile {
   int first, last;
 };
 
-// Tile `id` of this launch.  All values are wave-uniform scalars.
+// The tile at `id`, or at the block's next id that has one (id moves there).
+// All values are wave-uniform scalars.
 template <int MODE, int BM, int BN>
-__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const ExpertTable& tab, int id) {
+__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const ExpertTable& tab, int& id) {
   const int cols = MODE == kFwd ? a.N : a.K, tn = (cols + BN - 1) / BN;
   // dw: every expert has the same row tiles
   const int fw = full_tiles<BM>(a.N), sw = short_tiles<BM>(a.N);
-  const int full = (MODE == kDw ? a.E * fw : __builtin_amdgcn_readfirstlane(tab.first[0][a.E])) * tn;
-  const int shorts = (MODE == kDw ? a.E * sw : __builtin_amdgcn_readfirstlane(tab.first[1][a.E])) * tn;
+  const int full = (MODE == kDw ? fw : __builtin_amdgcn_readfirstlane(tab.first[0][a.E])) * tn;
+  const int shorts = (MODE == kDw ? sw : __builtin_amdgcn_readfirstlane(tab.first[1][a.E])) * tn;
   Tile t;
   t.e = -1;
-  const TileIndex x = xcd_order(id, full * a.splits, shorts * a.splits);
+  const TileIndex x = MODE == kDw ? spread_order(id, gridDim.x, a.E, full * a.splits, shorts * a.splits)
+                                  : xcd_order(id, full * a.splits, shorts * a.splits);
   if (x.at < 0) return t;
-  const int per = x.short_ ? shorts : full;
-  t.split = x.at / per;
-  const int at = x.at - t.split * per;
+  const int per = x.short_ ? shorts : full;      // dw: of one expert
   int tm, local;       // row tiles of this kind of the expert, index among its tiles of this kind
   if (MODE == kDw) {
     tm = x.short_ ? sw : fw;
-    t.e = at / (tm * tn);
-    local = at - t.e * tm * tn;
+    t.e = x.at / (per * a.splits);
+    const int in = x.at - t.e * per * a.splits;
+    t.split = in / per;
+    local = in - t.split * per;
   } else {
+    t.split = x.at / per;
+    const int at = x.at - t.split * per;
     const int* first = tab.first[x.short_ ? 1 : 0];
     const int q = at / tn, lane = threadIdx.x & 63;
     int e = -1;                                              // the last expert that starts at or before row tile q
@@ -528,7 +550,7 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
 
   // A tile with at most half of its rows runs at half the height: a good part
   // of the experts' last row tiles would otherwise multiply mostly nothing.
-  for (int id = blockIdx.x;; id += gridDim.x) {
+  for (int id = blockIdx.x;; id += gridDim.x) {   // find_tile may move id on
     const Tile t = find_tile<MODE, BM, BN>(a, tab, id);
     if (t.e < 0) break;
     if constexpr (NI == 8) {
