@@ -294,6 +294,13 @@ struct LinearPlan {
 };
 enum { kPlanGeneral = 0, kPlanFew, kPlanNarrow, kPlanTile128, kPlanTile256 };
 
+// Rows the streaming kernel plans an expert for: twice the average, or the
+// caller's bound (a fuller expert walks its weights again).
+inline int few_bound(const LinearArgs& a) {
+  const int twice = (a.rows + a.E - 1) / a.E * 2;
+  return a.E > 1 && twice < a.max_rows ? twice : a.max_rows;
+}
+
 LinearPlan plan_linear(int mode, const LinearArgs& a);
 int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
 int32_t launch_linear_general(int mode, int dtype, const LinearArgs& a, hipStream_t st);

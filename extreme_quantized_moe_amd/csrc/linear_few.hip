@@ -117,15 +117,18 @@ __global__ void __launch_bounds__(512) linear_narrow_kernel(LinearArgs a) {
 
 template <class T>
 static void run_few(const LinearArgs& a, hipStream_t st) {
-  // two column groups a block halve the traffic of x; with few columns in all
-  // one group and eight waves spread the weights over more of the chip
-  const int64_t groups = (int64_t)a.E * ((a.N + 31) / 32);
-  const bool wide = groups >= 1024;
+  // With few column groups in all, eight waves share one group of 16 columns.
+  // With many, four waves: two groups a block halve the traffic of x where the
+  // contraction is short (66 experts of 1408 x 2048 with 4 rows: 69 us against
+  // 78 with one), one group reads long rows faster (8 experts of 14336 x 4096
+  // with 4 rows: 174 us against 219 with two).
+  const bool wide = (int64_t)a.E * ((a.N + 31) / 32) >= 1024;
 #define RUN(MT, NT, NW)                                                                                        \
   hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E), dim3(64 * NW), \
                      0, st, a)
-  if (a.max_rows <= 16) { if (wide) RUN(1, 2, 4); else RUN(1, 1, 8); }
-  else if (a.max_rows <= 32) { if (wide) RUN(2, 2, 4); else RUN(2, 1, 8); }
+  const int bound = few_bound(a);
+  if (bound <= 16) { if (!wide) RUN(1, 1, 8); else if (a.K >= 4096) RUN(1, 1, 4); else RUN(1, 2, 4); }
+  else if (bound <= 32) { if (wide) RUN(2, 2, 4); else RUN(2, 1, 8); }
   else { if (wide) RUN(4, 2, 4); else RUN(4, 1, 8); }
 #undef RUN
 }

@@ -14,25 +14,34 @@ static bool wide_access(const LinearArgs& a) {
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Microseconds of a tile kernel, from what its steps (64 of the contraction)
-// and partial sums took on an MI355X: a step of a 256 x 256 tile 1.5; of a 128
-// x 128 tile 0.71 alone on its compute unit, 1.05 with a second block beside
-// it; the join of a split contraction 5, and its partial sums written and read
-// at 4 TB/s.  (512 x 4096 x 4096: 49 us unsplit, 38 in two, 35 in four parts
-// on 128 x 128 tiles; 8192 x 14336 x 4096: 936 us on 128 x 128, 700 on 256 x
-// 256 tiles.)
-static double tile_cost(int tile, int splits, int64_t tiles, int64_t steps, int64_t results, int64_t cus) {
+// Microseconds of a tile kernel, from what its steps (64 of the contraction),
+// results and partial sums took on an MI355X: a step of a 256 x 256 tile 1.5,
+// of a 128 x 128 tile 0.71 alone on its compute unit and 1.05 with a second
+// block beside it; a tile's results 8 and 3.5 in 16 bits, 13 and 7.4 in 32
+// (every compute unit writes at once); the join of a split contraction 5, and
+// its partial sums written and read at 4 TB/s.  Measured: 512 x 4096 x 4096 49
+// us unsplit, 38 in two, 35 in four parts on 128 x 128 tiles; 8192 x 14336 x
+// 4096 936 us on 128 x 128, 700 on 256 x 256 tiles; dw of 66 experts of 1408 x
+// 2048 with 31 rows on average 112 us on 128 x 128, 130 on 256 x 256 tiles, of
+// 8 experts of 4096 x 14336 with 512 rows 680 and 567.
+static double tile_cost(int tile, int splits, int64_t tiles, int64_t steps, int64_t results, bool wide_out,
+                        int64_t cus) {
   const int64_t work = tiles * splits;
-  double step;
+  const bool out32 = wide_out || splits > 1;
+  double step, out;
   int64_t rounds;
   if (tile == 256) {
     step = 1.5;
+    out = out32 ? 13 : 8;
     rounds = ceil_div(work, cus);
   } else {
     step = work <= cus ? 0.71 : 1.05;
+    out = out32 ? 7.4 : 3.5;
     rounds = work <= cus ? 1 : ceil_div(work, 2 * cus);
   }
-  return rounds * ceil_div(steps, splits) * step + (splits > 1 ? 5 + 8e-6 * splits * results / 4 : 0);
+  // fewer blocks than compute units write faster each
+  const double writes = rounds * out * (work < cus ? (double)work / cus : 1);
+  return rounds * ceil_div(steps, splits) * step + writes + (splits > 1 ? 5 + 4e-6 * splits * results / 4 : 0);
 }
 
 LinearPlan plan_linear(int mode, const LinearArgs& a) {
@@ -40,11 +49,14 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
   if (!wide_access(a)) return p;
   const int64_t rows = ceil_div(a.rows, a.E);            // of an expert, on average
   if (mode == kFwd) {
-    // Few rows an expert: the weights are streamed once for every 64 rows, at
-    // the memory's rate; from about 32 rows on a tile's reuse wins (4096 x
-    // 4096: 32 rows 14.7 us against 16.6 on split tiles, 64 rows 22.6 against
-    // 18.5).
-    if (a.max_rows <= 32 || rows <= 24) {
+    // Few rows an expert: the weights are streamed straight into the matrix
+    // cores.  Up to 8 rows on average always (64 rows over 8 experts of 14336 x
+    // 4096: 190 us, on tiles 210); up to 24 where the experts are small (66 of
+    // 1408 x 2048, 16 rows each: 85 us, on tiles 100) or too few tiles would
+    // run (24 x 4096 x 4096: 13 us, on tiles 17); large experts take tiles (12
+    // rows each of 8 x 14336 x 4096: 194 us, streamed 222).
+    if (few_bound(a) <= 16 ||
+        (rows <= 24 && ((int64_t)a.N * a.K <= kSmallMatrixElems || a.E * ceil_div(a.N, 128) < 256))) {
       p.kernel = kPlanFew;
       return p;
     }
@@ -62,7 +74,7 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
   for (int tile = 256; tile >= 128; tile -= 128)
     for (int splits = 1; splits <= 8 && (splits == 1 || 2 * splits <= steps); splits *= 2) {
       const int64_t tiles = a.E * ceil_div(m, tile) * ceil_div(n, tile);
-      const double c = tile_cost(tile, splits, tiles, steps, results, cus);
+      const double c = tile_cost(tile, splits, tiles, steps, results, a.out_f32, cus);
       if (p.kernel != kPlanGeneral && c >= best) continue;
       best = c;
       p.kernel = tile == 256 ? kPlanTile256 : kPlanTile128;
