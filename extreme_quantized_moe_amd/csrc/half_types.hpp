@@ -37,9 +37,10 @@ struct F32 {
 };
 
 // V consecutive elements, loaded and stored as one access (V sizeof(store)
-// bytes, aligned to that).
-template <class T, int V>
-struct alignas(V * sizeof(typename T::store)) Pack {
+// bytes, aligned to that).  LOOSE: aligned to one element only; the memory
+// system takes such accesses whole too, at a lower rate.
+template <class T, int V, bool LOOSE = false>
+struct alignas(LOOSE ? sizeof(typename T::store) : V * sizeof(typename T::store)) Pack {
   typename T::store v[V];
 };
 

@@ -223,64 +223,91 @@ __device__ __forceinline__ int64_t out_at(const LinearArgs& a, int e, int64_t ro
   return ((MODE == kDw ? (int64_t)e * a.N : 0) + row) * (MODE == kFwd ? a.N : a.K) + col;
 }
 
-template <class T, int V>
-__device__ __forceinline__ Pack<T, V> load_pack(const void* p, int64_t at) {
-  return *(const Pack<T, V>*)((const uint16_t*)p + at);
+template <class T, int V, bool LOOSE = false>
+__device__ __forceinline__ Pack<T, V, LOOSE> load_pack(const void* p, int64_t at) {
+  return *(const Pack<T, V, LOOSE>*)((const uint16_t*)p + at);
 }
 
-template <class T, int V>
-__device__ __forceinline__ void add_pack(float* v, const Pack<T, V>& p) {
+template <class T, int V, bool LOOSE>
+__device__ __forceinline__ void add_pack(float* v, const Pack<T, V, LOOSE>& p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] += T::up(p.v[i]);
 }
 
-template <class T, int V>
-__device__ __forceinline__ void mul_pack(float* v, const Pack<T, V>& p) {
+template <class T, int V, bool LOOSE>
+__device__ __forceinline__ void mul_pack(float* v, const Pack<T, V, LOOSE>& p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] *= T::up(p.v[i]);
 }
 
-template <class T, int V>
+template <class T, int V, bool LOOSE = false>
 __device__ __forceinline__ void store_pack(void* dst, int64_t at, const float* v) {
-  Pack<T, V> o;
+  Pack<T, V, LOOSE> o;
 #pragma unroll
   for (int i = 0; i < V; ++i) o.v[i] = T::down(v[i]);
-  *(Pack<T, V>*)((uint16_t*)dst + at) = o;
+  *(Pack<T, V, LOOSE>*)((uint16_t*)dst + at) = o;
 }
 
-template <class T, int V>
+template <class T, int V, bool LOOSE = false>
 __device__ __forceinline__ void store_out(const LinearArgs& a, int64_t at, const float* v) {
   if (a.out_f32) {
     constexpr int W = V < 4 ? V : 4;        // at most 16 bytes an access
 #pragma unroll
     for (int p = 0; p < V / W; ++p) {
-      Pack<F32, W> o;
+      Pack<F32, W, LOOSE> o;
 #pragma unroll
       for (int i = 0; i < W; ++i) o.v[i] = v[p * W + i];
-      *(Pack<F32, W>*)((float*)a.out + at + p * W) = o;
+      *(Pack<F32, W, LOOSE>*)((float*)a.out + at + p * W) = o;
     }
   } else {
-    store_pack<T, V>(a.out, at, v);
+    store_pack<T, V, LOOSE>(a.out, at, v);
   }
 }
 
-template <class T, int MODE, int V>
+template <class T, int MODE, int V, bool LOOSE = false>
 __device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, int col, const float* v_in) {
   const int64_t at = out_at<MODE>(a, e, row, col);
   float v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = v_in[i];
   if constexpr (MODE == kFwd) {
-    if (a.bias) add_pack<T, V>(v, load_pack<T, V>(a.bias, (int64_t)e * a.N + col));
-    if (a.pre) store_pack<T, V>(a.pre, at, v);
+    if (a.bias) add_pack(v, load_pack<T, V, LOOSE>(a.bias, (int64_t)e * a.N + col));
+    if (a.pre) store_pack<T, V, LOOSE>(a.pre, at, v);
     if (a.act != MILO_ACT_NONE) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = act_value(a.act, v[i]);
     }
-    if (a.mul) mul_pack<T, V>(v, load_pack<T, V>(a.mul, at));
+    if (a.mul) mul_pack(v, load_pack<T, V, LOOSE>(a.mul, at));
   }
-  if (MODE != kDw && a.residual) add_pack<T, V>(v, load_pack<T, V>(a.residual, at));
-  store_out<T, V>(a, at, v);
+  if (MODE != kDw && a.residual) add_pack(v, load_pack<T, V, LOOSE>(a.residual, at));
+  store_out<T, V, LOOSE>(a, at, v);
+}
+
+// V columns of one row, of which `left` are inside: whole, or one by one.
+template <class T, int MODE, int V>
+__device__ __forceinline__ void finish_loose(const LinearArgs& a, int e, int64_t row, int col, int left,
+                                             const float* v) {
+  if (left >= V) {
+    finish<T, MODE, V, true>(a, e, row, col, v);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < left; ++i) {
+      float one = v[0];
+#pragma unroll
+      for (int c = 1; c < V; ++c) one = i == c ? v[c] : one;   // a runtime index would put v in memory
+      finish<T, MODE, 1, true>(a, e, row, col + i, &one);
+    }
+  }
+}
+
+// 8 values at src of which `inside` are the operand's; the others read as zeros.
+__device__ __forceinline__ u32x4 load_loose(const uint16_t* src, int inside) {
+  typedef Pack<F16, 8, true> P;
+  if (inside >= 8) return __builtin_bit_cast(u32x4, *(const P*)src);
+  P p;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p.v[i] = i < inside ? src[i] : (uint16_t)0;
+  return __builtin_bit_cast(u32x4, p);
 }
 
 // ---------------------------------------------------------------- host side
@@ -290,9 +317,10 @@ constexpr int kLinearStep = 64;   // contraction values per step of the tile ker
 struct LinearPlan {
   int kernel;          // kPlan*
   int splits;
+  int loose;           // element-aligned operands or odd row lengths
   size_t part_bytes;   // fp32 partial sums of a split contraction
 };
-enum { kPlanGeneral = 0, kPlanFew, kPlanNarrow, kPlanTile128, kPlanTile256 };
+enum { kPlanFew = 0, kPlanNarrow, kPlanTile128, kPlanTile256 };
 
 // Rows the streaming kernel plans an expert for: twice the average, or the
 // caller's bound (a fuller expert walks its weights again).
@@ -303,10 +331,10 @@ inline int few_bound(const LinearArgs& a) {
 
 LinearPlan plan_linear(int mode, const LinearArgs& a);
 int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
-int32_t launch_linear_general(int mode, int dtype, const LinearArgs& a, hipStream_t st);
 int32_t launch_linear_tile(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st);
-int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, hipStream_t st);
-int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, hipStream_t st);
+int32_t launch_linear_loose(int mode, int dtype, const LinearArgs& a, hipStream_t st);
+int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, bool loose, hipStream_t st);
+int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, bool loose, hipStream_t st);
 size_t act_grad_workspace_bytes(int E, int N, int rows);
 int32_t launch_act_grad(const void* dy, const void* pre, const void* mul, const int32_t* offsets, int E, int N,
                         int rows, int dtype, int act, void* dpre, void* dmul, float* dbias, float* part,

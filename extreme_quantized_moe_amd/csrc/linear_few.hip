@@ -9,7 +9,9 @@
 // A lane's operand: row l % 16, contraction values 8 (l / 16) .. +7 of a step
 // of 32: 16-byte loads, 64 contiguous bytes a row and load, four loads to 256.
 // Rows of x past the expert's and columns past N are cut off by the buffer
-// resources' ends: they read as zeros and cost no traffic.
+// resources' ends: they read as zeros and cost no traffic.  LOOSE: operands
+// aligned to their elements only or odd row lengths, through plain loads with
+// the same bounds.
 #include "linear.hpp"
 
 namespace milo {
@@ -18,7 +20,7 @@ constexpr int kFewRsrcWord3 = 0x00020000;
 constexpr int kFewOutside = 0x7FFFFFF0;
 constexpr int kFewPiece = 128;            // contraction values a wave takes at a time
 
-template <class T, int MT, int NT, int NW>
+template <class T, int MT, int NT, int NW, bool LOOSE>
 __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, int m0, int rows, int n0, float* lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = a.K, left_n = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT;
@@ -35,7 +37,23 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
   auto load = [&](int k0, Piece& p) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const bool in = k0 + 32 * s + 8 * (lane >> 4) < K;
+      const int k = k0 + 32 * s + 8 * (lane >> 4);
+      const bool in = k < K;
+      if constexpr (LOOSE) {
+        const uint16_t* w = (const uint16_t*)a.b + ((int64_t)e * a.N + n0) * K + k;
+        const uint16_t* x = (const uint16_t*)a.a + (int64_t)(base + m0) * K + k;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int r = 16 * t + (lane & 15);
+          p.w[t][s] = load_loose(w + (int64_t)r * K, r < left_n ? K - k : 0);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const int r = 16 * t + (lane & 15);
+          p.x[t][s] = load_loose(x + (int64_t)r * K, r < left_m ? K - k : 0);
+        }
+        continue;
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         p.w[t][s] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? at + (16 * t * K + k0 + 32 * s) * 2 : kFewOutside, 0, 0);
@@ -80,13 +98,14 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
 #pragma unroll
     for (int w = 1; w < NW; ++w) sum += *(const f32x4*)(lds + (w * 16 * MT + r) * kLine + c);
     const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    finish<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, v);
+    if constexpr (LOOSE) finish_loose<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, a.N - n0 - c, v);
+    else finish<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, v);
   }
 }
 
 // MT_MAX bounds the 16-row groups of one walk; an expert with fewer rows takes
 // the smallest form that holds them.
-template <class T, int MT_MAX, int NT, int NW>
+template <class T, int MT_MAX, int NT, int NW, bool LOOSE>
 __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   __shared__ __align__(16) float lds[NW * 16 * MT_MAX * (16 * NT + 4)];
@@ -94,9 +113,9 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
   const Span s = expert_span(a.offsets, e, a.rows);
   for (int m0 = 0; m0 < s.rows; m0 += 16 * MT_MAX) {
     const int left = s.rows - m0;
-    if (left <= 16 || MT_MAX == 1) few_rows<T, 1, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
-    else if (left <= 32 || MT_MAX == 2) few_rows<T, MT_MAX < 2 ? 1 : 2, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
-    else few_rows<T, MT_MAX, NT, NW>(a, e, s.base, m0, s.rows, n0, lds);
+    if (left <= 16 || MT_MAX == 1) few_rows<T, 1, NT, NW, LOOSE>(a, e, s.base, m0, s.rows, n0, lds);
+    else if (left <= 32 || MT_MAX == 2) few_rows<T, MT_MAX < 2 ? 1 : 2, NT, NW, LOOSE>(a, e, s.base, m0, s.rows, n0, lds);
+    else few_rows<T, MT_MAX, NT, NW, LOOSE>(a, e, s.base, m0, s.rows, n0, lds);
   }
 #endif
 }
@@ -104,18 +123,18 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 // The same walk for few columns and many rows (a router): a block takes 16
 // rows and 64 columns, so it is x that is streamed once and w that every
 // block reads again, from the L2.
-template <class T>
+template <class T, bool LOOSE>
 __global__ void __launch_bounds__(512) linear_narrow_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   __shared__ __align__(16) float lds[8 * 16 * (64 + 4)];
   const int id = blockIdx.x, width = (a.N + 63) / 64;
   const TileSlot s = find_slot(a.offsets, a.E, a.rows, 16, width, [&](int) { return id; });
   if (s.e < 0) return;
-  few_rows<T, 1, 4, 8>(a, s.e, s.span.base, s.local / width * 16, s.span.rows, s.local % width * 64, lds);
+  few_rows<T, 1, 4, 8, LOOSE>(a, s.e, s.span.base, s.local / width * 16, s.span.rows, s.local % width * 64, lds);
 #endif
 }
 
-template <class T>
+template <class T, bool LOOSE>
 static void run_few(const LinearArgs& a, hipStream_t st) {
   // With few column groups in all, eight waves share one group of 16 columns.
   // With many, four waves: two groups a block halve the traffic of x where the
@@ -124,8 +143,8 @@ static void run_few(const LinearArgs& a, hipStream_t st) {
   // with 4 rows: 174 us against 219 with two).
   const bool wide = (int64_t)a.E * ((a.N + 31) / 32) >= 1024;
 #define RUN(MT, NT, NW)                                                                                        \
-  hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E), dim3(64 * NW), \
-                     0, st, a)
+  hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW, LOOSE>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E),      \
+                     dim3(64 * NW), 0, st, a)
   const int bound = few_bound(a);
   if (bound <= 16) { if (!wide) RUN(1, 1, 8); else if (a.K >= 4096) RUN(1, 1, 4); else RUN(1, 2, 4); }
   else if (bound <= 32) { if (wide) RUN(2, 2, 4); else RUN(2, 1, 8); }
@@ -133,15 +152,21 @@ static void run_few(const LinearArgs& a, hipStream_t st) {
 #undef RUN
 }
 
-template <class T>
+template <class T, bool LOOSE>
 static void run_narrow(const LinearArgs& a, hipStream_t st) {
   const int64_t blocks = ((int64_t)(a.rows + 15) / 16 + (a.E > 1 ? a.E : 0)) * ((a.N + 63) / 64);
-  hipLaunchKernelGGL(linear_narrow_kernel<T>, dim3((unsigned)blocks), dim3(512), 0, st, a);
+  hipLaunchKernelGGL((linear_narrow_kernel<T, LOOSE>), dim3((unsigned)blocks), dim3(512), 0, st, a);
 }
 
-int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, hipStream_t st) {
-  if (dtype == MILO_F16) { if (narrow) run_narrow<F16>(a, st); else run_few<F16>(a, st); }
-  else { if (narrow) run_narrow<BF16>(a, st); else run_few<BF16>(a, st); }
+template <class T>
+static void run_any(const LinearArgs& a, bool narrow, bool loose, hipStream_t st) {
+  if (narrow) { if (loose) run_narrow<T, true>(a, st); else run_narrow<T, false>(a, st); }
+  else { if (loose) run_few<T, true>(a, st); else run_few<T, false>(a, st); }
+}
+
+int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, bool loose, hipStream_t st) {
+  if (dtype == MILO_F16) run_any<F16>(a, narrow, loose, st);
+  else run_any<BF16>(a, narrow, loose, st);
   return hip_status(hipGetLastError(), "linear_few_kernel launch");
 }
 

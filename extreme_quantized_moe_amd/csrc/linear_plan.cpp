@@ -5,7 +5,7 @@
 namespace milo {
 
 // 16-byte accesses everywhere: row lengths of a multiple of 8 elements and
-// 16-byte aligned arrays; anything else takes the general kernel.
+// 16-byte aligned arrays; anything else takes the loose forms.
 static bool wide_access(const LinearArgs& a) {
   const uintptr_t bits = (uintptr_t)a.a | (uintptr_t)a.b | (uintptr_t)a.bias | (uintptr_t)a.mul |
                          (uintptr_t)a.residual | (uintptr_t)a.pre | (uintptr_t)a.out;
@@ -45,8 +45,7 @@ static double tile_cost(int tile, int splits, int64_t tiles, int64_t steps, int6
 }
 
 LinearPlan plan_linear(int mode, const LinearArgs& a) {
-  LinearPlan p = {kPlanGeneral, 1, 0};
-  if (!wide_access(a)) return p;
+  LinearPlan p = {kPlanTile128, 1, !wide_access(a), 0};
   const int64_t rows = ceil_div(a.rows, a.E);            // of an expert, on average
   if (mode == kFwd) {
     // Few rows an expert: the weights are streamed straight into the matrix
@@ -54,9 +53,11 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
     // 4096: 190 us, on tiles 210); up to 24 where the experts are small (66 of
     // 1408 x 2048, 16 rows each: 85 us, on tiles 100) or too few tiles would
     // run (24 x 4096 x 4096: 13 us, on tiles 17); large experts take tiles (12
-    // rows each of 8 x 14336 x 4096: 194 us, streamed 222).
-    if (few_bound(a) <= 16 ||
-        (rows <= 24 && ((int64_t)a.N * a.K <= kSmallMatrixElems || a.E * ceil_div(a.N, 128) < 256))) {
+    // rows each of 8 x 14336 x 4096: 194 us, streamed 222), at odd row lengths
+    // from the first row on (4 rows each of 8 x 14335 x 4097: 321 us, streamed 493).
+    const bool few_tiles = a.E * ceil_div(a.N, 128) < 256;
+    if ((few_bound(a) <= 16 && (!p.loose || few_tiles)) ||
+        (rows <= 24 && (few_tiles || (!p.loose && (int64_t)a.N * a.K <= kSmallMatrixElems)))) {
       p.kernel = kPlanFew;
       return p;
     }
@@ -71,11 +72,13 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
   const int64_t depth = mode == kFwd ? a.K : mode == kDx ? a.N : rows, steps = ceil_div(depth, kLinearStep);
   const int64_t results = (mode == kDw ? (int64_t)a.E * a.N : a.rows) * n, cus = device_cu_count();
   double best = 0;
-  for (int tile = 256; tile >= 128; tile -= 128)
+  bool any = false;
+  for (int tile = p.loose ? 128 : 256; tile >= 128; tile -= 128)
     for (int splits = 1; splits <= 8 && (splits == 1 || 2 * splits <= steps); splits *= 2) {
       const int64_t tiles = a.E * ceil_div(m, tile) * ceil_div(n, tile);
       const double c = tile_cost(tile, splits, tiles, steps, results, a.out_f32, cus);
-      if (p.kernel != kPlanGeneral && c >= best) continue;
+      if (any && c >= best) continue;
+      any = true;
       best = c;
       p.kernel = tile == 256 ? kPlanTile256 : kPlanTile128;
       p.splits = splits;
@@ -85,13 +88,12 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
 }
 
 int32_t launch_linear(int mode, int dtype, const LinearArgs& args, const LinearPlan& p, hipStream_t st) {
-  if (p.kernel == kPlanGeneral) return launch_linear_general(mode, dtype, args, st);
   if (p.kernel == kPlanFew || p.kernel == kPlanNarrow)
-    return launch_linear_few(dtype, args, p.kernel == kPlanNarrow, st);
+    return launch_linear_few(dtype, args, p.kernel == kPlanNarrow, p.loose, st);
   LinearArgs a = args;
   a.splits = p.splits;
-  const int32_t rc = launch_linear_tile(mode, dtype, a, p.kernel, st);
-  return rc || p.splits == 1 ? rc : launch_linear_join(mode, dtype, a, st);
+  const int32_t rc = p.loose ? launch_linear_loose(mode, dtype, a, st) : launch_linear_tile(mode, dtype, a, p.kernel, st);
+  return rc || p.splits == 1 ? rc : launch_linear_join(mode, dtype, a, p.loose, st);
 }
 
 }  // namespace milo

@@ -45,7 +45,7 @@ static hipError_t run_type(int mode, const LinearArgs& a, int kernel, hipStream_
 
 // ---- split contraction: the partial sums of each result in split order, then
 // the epilogue.  A wave takes one row, a lane 8 columns.
-template <class T, int MODE>
+template <class T, int MODE, bool LOOSE>
 __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a) {
   const int cols = MODE == kFwd ? a.N : a.K;
   const int n = (blockIdx.y * 64 + (threadIdx.x & 63)) * 8, wave = threadIdx.x >> 6;
@@ -65,33 +65,44 @@ __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a) {
   }
   if (n >= cols) return;
   const int64_t one = (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols, at = out_at<MODE>(a, e, row, n);
-  f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < a.splits; ++s) {
-    lo += *(const f32x4*)(a.part + s * one + at);
-    hi += *(const f32x4*)(a.part + s * one + at + 4);
+    const float* p = a.part + s * one + at;
+    if constexpr (LOOSE) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += n + c < cols ? p[c] : 0.f;
+    } else {
+      const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 4);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] += lo[c];
+        v[4 + c] += hi[c];
+      }
+    }
   }
-  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  finish<T, MODE, 8>(a, e, row, n, v);
+  if constexpr (LOOSE) finish_loose<T, MODE, 8>(a, e, row, n, cols - n, v);
+  else finish<T, MODE, 8>(a, e, row, n, v);
 }
 
 template <class T, int MODE>
-static void run_join(const LinearArgs& a, hipStream_t st) {
+static void run_join(const LinearArgs& a, bool loose, hipStream_t st) {
   const int cols = MODE == kFwd ? a.N : a.K;
   const int64_t quads = MODE == kDw ? ((int64_t)a.E * a.N + 3) / 4 : (a.rows + 3) / 4 + (a.E > 1 ? a.E : 0);
-  hipLaunchKernelGGL((linear_join_kernel<T, MODE>), dim3((unsigned)quads, (unsigned)((cols + 511) / 512)), dim3(256),
-                     0, st, a);
+  const dim3 grid((unsigned)quads, (unsigned)((cols + 511) / 512));
+  if (loose) hipLaunchKernelGGL((linear_join_kernel<T, MODE, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((linear_join_kernel<T, MODE, false>), grid, dim3(256), 0, st, a);
 }
 
 template <class T>
-static void run_join_mode(int mode, const LinearArgs& a, hipStream_t st) {
-  if (mode == kFwd) run_join<T, kFwd>(a, st);
-  else if (mode == kDx) run_join<T, kDx>(a, st);
-  else run_join<T, kDw>(a, st);
+static void run_join_mode(int mode, const LinearArgs& a, bool loose, hipStream_t st) {
+  if (mode == kFwd) run_join<T, kFwd>(a, loose, st);
+  else if (mode == kDx) run_join<T, kDx>(a, loose, st);
+  else run_join<T, kDw>(a, loose, st);
 }
 
-int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, hipStream_t st) {
-  if (dtype == MILO_F16) run_join_mode<F16>(mode, a, st);
-  else run_join_mode<BF16>(mode, a, st);
+int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, bool loose, hipStream_t st) {
+  if (dtype == MILO_F16) run_join_mode<F16>(mode, a, loose, st);
+  else run_join_mode<BF16>(mode, a, loose, st);
   return hip_status(hipGetLastError(), "linear_join_kernel launch");
 }
 

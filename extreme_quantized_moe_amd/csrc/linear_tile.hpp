@@ -287,7 +287,7 @@ __device__ __forceinline__ void swap_odd_even_rows(float& x, float& y) {
 }
 
 template <class T>
-using Packed8 = Pack<T, 8>;
+using Packed8 = Pack<T, 8, false>;
 
 // 8 values rounded to the 16-bit type.
 template <class T>
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
           }
           const int off = (n + 32 * j < cols ? 2 * at + 64 * j : kOutside) + 32 * g * cols;
           if constexpr (MODE == kFwd) {
-            if (a.bias) add_pack<T, 8>(v, bias[j]);
+            if (a.bias) add_pack(v, bias[j]);
             if (a.pre) __builtin_amdgcn_raw_buffer_store_b128(rounded<T>(v), rp, off, 0, 0);
             if (ACT != MILO_ACT_NONE) {
 #pragma unroll
@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
 #pragma unroll
               for (int c = 0; c < 8; ++c) v[c] = act_value(MILO_ACT_RELU, v[c]);
             }
-            if (has_mul) mul_pack<T, 8>(v, __builtin_bit_cast(Packed8<T>, mul[i][j]));
+            if (has_mul) mul_pack(v, __builtin_bit_cast(Packed8<T>, mul[i][j]));
           }
-          if (has_add) add_pack<T, 8>(v, __builtin_bit_cast(Packed8<T>, add[i][j]));
+          if (has_add) add_pack(v, __builtin_bit_cast(Packed8<T>, add[i][j]));
           if (MODE != kFwd || !a.out_f32) {
             __builtin_amdgcn_raw_buffer_store_b128(rounded<T>(v), ro, off, 0, 0);
           } else {

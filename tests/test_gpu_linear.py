@@ -40,6 +40,8 @@ SHAPES = [
     ([17, 1, 40, 0, 64], 136, 200), ([70, 0, 129, 3], 264, 328), ([31, 33], 129, 127), ([256, 256], 256, 256),
     ([300, 1, 520], 384, 192), ([5] * 66, 72, 64), ([2, 0, 1] * 40, 24, 16), ([1000, 24], 512, 1032),
     ([15, 16, 17, 31, 32, 33], 2056, 1096), ([700], 1024, 2048), ([90, 40], 5000, 64),
+    ([300, 0, 200], 515, 1031), ([700], 331, 2049), ([4, 1, 9], 1001, 4099), ([1], 4097, 130), ([200], 50, 1999),
+    ([100], 384, 4096), ([129, 385], 264, 1544),
 ]
 EPILOGUES = [  # bias, activation, mul, residual, out fp32, keep
     (False, "none", False, False, False, False), (True, "relu", False, True, False, True),
