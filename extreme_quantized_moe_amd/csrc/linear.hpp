@@ -322,6 +322,8 @@ struct LinearPlan {
 };
 enum { kPlanFew = 0, kPlanNarrow, kPlanTile128, kPlanTile256 };
 
+constexpr int kFewWalks = 8;      // walks of 16 rows that blocks of the streaming kernel share
+
 // Rows the streaming kernel plans an expert for: twice the average, or the
 // caller's bound (a fuller expert walks its weights again).
 inline int few_bound(const LinearArgs& a) {

@@ -12,6 +12,8 @@
 // resources' ends: they read as zeros and cost no traffic.  LOOSE: operands
 // aligned to their elements only or odd row lengths, through plain loads with
 // the same bounds.
+#include <algorithm>
+
 #include "linear.hpp"
 
 namespace milo {
@@ -104,14 +106,17 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
 }
 
 // MT_MAX bounds the 16-row groups of one walk; an expert with fewer rows takes
-// the smallest form that holds them.
+// the smallest form that holds them.  Blocks along z share the walks of an
+// expert that needs more than one (skewed routing: 128 rows over 66 experts of
+// 1408 x 2048, 74 of them one expert's, 52 us with one block to a column
+// group, 25 with one to a walk; balanced ones lose nothing to the empty blocks).
 template <class T, int MT_MAX, int NT, int NW, bool LOOSE>
 __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   __shared__ __align__(16) float lds[NW * 16 * MT_MAX * (16 * NT + 4)];
   const int e = blockIdx.y, n0 = blockIdx.x * 16 * NT;
   const Span s = expert_span(a.offsets, e, a.rows);
-  for (int m0 = 0; m0 < s.rows; m0 += 16 * MT_MAX) {
+  for (int m0 = 16 * MT_MAX * blockIdx.z; m0 < s.rows; m0 += 16 * MT_MAX * gridDim.z) {
     const int left = s.rows - m0;
     if (left <= 16 || MT_MAX == 1) few_rows<T, 1, NT, NW, LOOSE>(a, e, s.base, m0, s.rows, n0, lds);
     else if (left <= 32 || MT_MAX == 2) few_rows<T, MT_MAX < 2 ? 1 : 2, NT, NW, LOOSE>(a, e, s.base, m0, s.rows, n0, lds);
@@ -142,8 +147,9 @@ static void run_few(const LinearArgs& a, hipStream_t st) {
   // 78 with one), one group reads long rows faster (8 experts of 14336 x 4096
   // with 4 rows: 174 us against 219 with two).
   const bool wide = (int64_t)a.E * ((a.N + 31) / 32) >= 1024;
-#define RUN(MT, NT, NW)                                                                                        \
-  hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW, LOOSE>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E),      \
+  auto walks = [&](int mt) { return std::min(kFewWalks, (a.max_rows + 16 * mt - 1) / (16 * mt)); };
+#define RUN(MT, NT, NW)                                                                                         \
+  hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, NW, LOOSE>), dim3((a.N + 16 * NT - 1) / (16 * NT), a.E, walks(MT)), \
                      dim3(64 * NW), 0, st, a)
   const int bound = few_bound(a);
   if (bound <= 16) { if (!wide) RUN(1, 1, 8); else if (a.K >= 4096) RUN(1, 1, 4); else RUN(1, 2, 4); }

@@ -49,15 +49,16 @@ LinearPlan plan_linear(int mode, const LinearArgs& a) {
   const int64_t rows = ceil_div(a.rows, a.E);            // of an expert, on average
   if (mode == kFwd) {
     // Few rows an expert: the weights are streamed straight into the matrix
-    // cores.  Up to 8 rows on average always (64 rows over 8 experts of 14336 x
-    // 4096: 190 us, on tiles 210); up to 24 where the experts are small (66 of
-    // 1408 x 2048, 16 rows each: 85 us, on tiles 100) or too few tiles would
-    // run (24 x 4096 x 4096: 13 us, on tiles 17); large experts take tiles (12
-    // rows each of 8 x 14336 x 4096: 194 us, streamed 222), at odd row lengths
-    // from the first row on (4 rows each of 8 x 14335 x 4097: 321 us, streamed 493).
-    const bool few_tiles = a.E * ceil_div(a.N, 128) < 256;
-    if ((few_bound(a) <= 16 && (!p.loose || few_tiles)) ||
-        (rows <= 24 && (few_tiles || (!p.loose && (int64_t)a.N * a.K <= kSmallMatrixElems)))) {
+    // cores, where no expert can have many (an expert's further rows read its
+    // weights again: 500 rows over 66 experts of 1408 x 2048, 305 of them one
+    // expert's, 66 us, on tiles 29) and either few rows are certain (32 over 8
+    // experts of 14336 x 4096: 168 us, on tiles 174), the experts are small (66
+    // of 1408 x 2048, 16 rows each: 85 us, on tiles 100) or few tiles would run
+    // (24 x 4096 x 4096: 13 us, on tiles 17).  Large experts take tiles (12
+    // rows each of 8 x 14336 x 4096: 194 us, streamed 222), and so do odd row
+    // lengths (4 rows each of 8 x 14335 x 4097: 321 us, streamed 493).
+    const bool few_tiles = a.E * ceil_div(a.N, 128) < 256, small = (int64_t)a.N * a.K <= kSmallMatrixElems;
+    if (rows <= 24 && a.max_rows <= 16 * kFewWalks && (few_tiles || ((a.max_rows <= 32 || small) && !p.loose))) {
       p.kernel = kPlanFew;
       return p;
     }

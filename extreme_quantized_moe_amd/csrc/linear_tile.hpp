@@ -24,7 +24,7 @@ namespace milo {
 
 constexpr int kDepth = kLinearStep;        // contraction values per step
 constexpr int kTileRsrcWord3 = 0x00020000; // raw buffer, bounds checked in bytes
-constexpr int kOutside = 0x7FFFFFF0;       // an offset no operand reaches
+constexpr int kOutside = 0x70000000;       // an offset no operand reaches, with room for a tile's offsets after it
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -561,6 +561,8 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
     }
     tile(t, std::integral_constant<int, NI>());
   }
+  // the loads past the last step (of nothing) have ended before the LDS is given back
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #endif
 }
 
