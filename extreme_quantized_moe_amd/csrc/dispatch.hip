@@ -167,9 +167,12 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float* __restrict
     g[c] = 0.f;
     pick[c] = false;
   }
+  // lane j holds pick j: the picks are one load, not one after the other
+  const int my_id = lane < k ? ids[t * k + lane] : -1;
+  const float my_g = lane < k ? dslot_w[t * slots + lane] : 0.f;
   for (int j = 0; j < k; ++j) {
-    const int id = ids[t * k + j];
-    const float gj = dslot_w[t * slots + j];
+    const int id = __shfl(my_id, j);
+    const float gj = __shfl(my_g, j);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (64 * c + lane == id) {
