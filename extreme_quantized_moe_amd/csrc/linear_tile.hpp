@@ -137,6 +137,14 @@ __device__ __forceinline__ TileIndex xcd_order(int id, int full, int shorts) {
   const int x = id & 7;
   int i = id >> 3;
   const int nf = (full >> 3) + (x < (full & 7) ? 1 : 0), ns = (shorts >> 3) + (x < (shorts & 7) ? 1 : 0);
+  const int step = gridDim.x >> 3, l = i % step, j = i / step;
+  // Every other block starts with its last tile, often a short one: their
+  // results' traffic then falls between the others', not all at once (SiLU,
+  // gate operand and kept pre-activation on those rows: 985 us, 964 so).
+  if ((l & 1) && i < nf + ns) {
+    const int c = (nf + ns - l + step - 1) / step;
+    i = l + (j == 0 ? c - 1 : j - 1) * step;
+  }
   if (i < nf) return {x * (full >> 3) + min(x, full & 7) + i, false};
   i -= nf;
   if (i < ns) return {x * (shorts >> 3) + min(x, shorts & 7) + i, true};
