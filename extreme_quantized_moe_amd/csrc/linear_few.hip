@@ -4,7 +4,10 @@
 // pieces of 128 with the next piece's loads in flight, straight from memory
 // into matrix-core operands (no LDS on the way: a weight is used once).  Row
 // counts up to 16 MT go in one walk; more rows walk again, 16 MT at a time.
-// Partial sums meet in LDS in wave order.
+// Partial sums meet in LDS in wave order.  Measured: one row of 4096 x 14336
+// 19.4 us (6.1 TB/s), 32 rows over 8 experts of 14336 x 4096 160..175 us (5.4 to
+// 5.9 TB/s).  Loads that pass the caches by (non-temporal) were slower: 199 us
+// against 170 for 16 rows over 8 experts of 4096 x 14336.
 //
 // A lane's operand: row l % 16, contraction values 8 (l / 16) .. +7 of a step
 // of 32: 16-byte loads, 64 contiguous bytes a row and load, four loads to 256.
@@ -127,7 +130,8 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 
 // The same walk for few columns and many rows (a router): a block takes 16
 // rows and 64 columns, so it is x that is streamed once and w that every
-// block reads again, from the L2.
+// block reads again, from the L2, which bounds it: 4096 rows of 2048 to 64
+// columns 13 us (x alone would take 4).
 template <class T, bool LOOSE>
 __global__ void __launch_bounds__(512) linear_narrow_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
