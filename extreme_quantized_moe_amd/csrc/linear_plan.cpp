@@ -19,7 +19,7 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // of a 128 x 128 tile 0.71 alone on its compute unit and 1.05 with a second
 // block beside it; a tile's results 8 and 3.5 in 16 bits, 13 and 7.4 in 32
 // (every compute unit writes at once); the join of a split contraction 5, and
-// its partial sums written and read at 4 TB/s.  Measured: 512 x 4096 x 4096 49
+// its reading of the partial sums 4 TB/s.  Measured: 512 x 4096 x 4096 49
 // us unsplit, 38 in two, 35 in four parts on 128 x 128 tiles; 8192 x 14336 x
 // 4096 936 us on 128 x 128, 700 on 256 x 256 tiles; dw of 66 experts of 1408 x
 // 2048 with 31 rows on average 112 us on 128 x 128, 130 on 256 x 256 tiles, of

@@ -241,7 +241,8 @@ def moe_linear_act_grad(dy, pre, activation, mul=None, offsets=None, num_experts
     """Gradient through `moe_linear`'s epilogue: (dpre, dmul, dbias) with
     dpre = dy * mul * act'(pre), dmul = dy * act(pre) (None without mul) and
     dbias fp32 [E][N], the sum of dpre over each expert's rows (None unless
-    bias_grad).  The residual's gradient is dy itself."""
+    bias_grad).  The residual's gradient is dy itself.  Rows outside the
+    offsets are not written (uninitialised)."""
     code = _float_type("dy", dy, wide=False)
     _need(dy.dim() == 2, "dy must be [rows][N]")
     dev, dt = dy.device, dy.dtype
@@ -266,7 +267,8 @@ def moe_linear_grad(dy, x, w, offsets=None, need_dx=True, need_dw=True, dw_dtype
     """Gradients of the product: (dx [rows][K] = dy w[e], dw like w = sum over
     each expert's rows of dy^T x), None where not needed.  dw in x's type or
     dw_dtype float32.  dx_add [rows][K]: added to dx in fp32 before its
-    rounding (the gradient of the same x from another product)."""
+    rounding (the gradient of the same x from another product).  Rows of dx
+    outside the offsets are not written (uninitialised)."""
     code = _float_type("dy", dy, wide=False)
     _need(dy.dim() == 2 and x.dim() == 2, "dy must be [rows][N] and x [rows][K]")
     dev, dt = dy.device, dy.dtype
@@ -304,9 +306,12 @@ class MoELayer16:
         self.E, self.k, self.S, self.renormalize = E, k, S, renormalize
 
     def forward(self, x, logits, keep=False):
-        """out [T][H]; with keep also what `backward` takes."""
+        """x [T][H] and float32 logits [T][E] to out [T][H]; with keep also what
+        `backward` takes."""
         T, slots = x.shape[0], self.k + self.S
-        r = route_sort(logits, self.k, self.S, self.renormalize)
+        logits = logits.contiguous()
+        _tensor("logits", logits, torch.float32, (T, self.E), self.w1.device)
+        r = route_sort(logits, self.k, self.S, self.renormalize, own_scratch=True)
         off = r["offsets"]
         xs = moe_permute(x, r["pair_pos"], slots)
         up = moe_linear(xs, self.w3, off, max_rows_per_expert=T)

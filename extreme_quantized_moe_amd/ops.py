@@ -196,10 +196,11 @@ def rank_policy(kurtosis, frequency, dense, total_rank, r_min=0, r_max=64, step=
 _route_ws = {}
 
 
-def route_sort(logits, k, S=0, renormalize=True):
+def route_sort(logits, k, S=0, renormalize=True, own_scratch=False):
     """Softmax top-k routing + expert sort.  Returns dict of device tensors:
     ids [T][k], w [T][k], slot_w [T*(k+S)], sorted_pairs, pair_pos [T*(k+S)],
-    offsets [E+S+1]."""
+    offsets [E+S+1].  own_scratch: scratch of this call's own instead of the
+    device's kept one (calls that overlap: several streams or graphs)."""
     logits = logits.contiguous()
     _cuda(logits)
     T, E = logits.shape
@@ -215,7 +216,9 @@ def route_sort(logits, k, S=0, renormalize=True):
     }
     nbytes = int(L.lib().milo_route_workspace_bytes(T, E, k, S))
     ws = None
-    if nbytes:
+    if nbytes and own_scratch:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif nbytes:
         key = (dev.index, nbytes)
         ws = _route_ws.get(key)
         if ws is None:

@@ -534,8 +534,8 @@ enum { MILO_F16 = 0, MILO_BF16 = 1, MILO_F32 = 2 };
  * slot_w  : float32 [T*slots], or NULL for weights of 1.
  * dslot_w : out, float32 [T*slots], or NULL (not computed).
  * Constraints: 0 <= T <= 2^24, 1 <= slots <= 16, 1 <= H <= 2^20,
- * 0 <= num_rows <= 2^28; pointers aligned to their element (16 bytes where
- * H rows of 16-byte multiples are to move at full speed).  T == 0 does nothing.
+ * 0 <= num_rows <= 2^28; pointers aligned to their element (rows of a multiple
+ * of 16 bytes in 16-byte aligned buffers move fastest).  T == 0 does nothing.
  * Pointers of buffers without an element may be NULL.
  */
 int32_t milo_moe_permute(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,

@@ -297,3 +297,50 @@ def test_binding_refusals():
         m.moe_linear_act_grad(x, x[:4], "silu")
     with pytest.raises(ValueError):
         m.moe_permute(x, off, 3)
+
+
+@pytest.mark.parametrize("E", [1, 5])
+@pytest.mark.parametrize("N,K", [(64, 128), (33, 17)])
+def test_no_rows_at_all(E, N, K):
+    """A buffer without a row: outputs without a row, weight and bias gradients of zeros."""
+    m = _m()
+    dt = torch.bfloat16
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    x, w, dy = rand((0, K), dt, 1), rand((E, N, K), dt, 2), rand((0, N), dt, 3)
+    assert m.moe_linear(x, w, off, activation="silu").shape == (0, N)
+    dx, dw = m.moe_linear_grad(dy, x, w, off, dw_dtype=torch.float32)
+    assert dx.shape == (0, K) and torch.equal(dw, torch.zeros_like(dw))
+    dpre, _, dbias = m.moe_linear_act_grad(dy, dy, "gelu", offsets=off, bias_grad=True)
+    assert dpre.shape == (0, N) and torch.equal(dbias, torch.zeros((E, N), device="cuda"))
+
+
+@pytest.mark.parametrize("counts,N,K", [([9, 0, 3], 512, 1024), ([700], 64, 1024), ([100], 384, 4096), ([900, 40, 0, 800], 2048, 512),
+                                        ([2100, 2000], 2048, 192), ([150, 3], 131, 1031), ([200], 50, 1999)])
+def test_every_form_captured(counts, N, K):
+    """Streaming, router, split, tile and loose forms in a graph, replayed with
+    other inputs between eager calls."""
+    m = _m()
+    dt = torch.bfloat16
+    off, dev = table(counts)
+    R, E = off[-1], len(counts)
+    x, w, dy = rand((R, K), dt, 1), rand((E, N, K), dt, 2, K ** -0.5), rand((R, N), dt, 3)
+
+    def step():
+        y, pre = m.moe_linear(x, w, dev, activation="gelu", residual=dy, return_pre=True)
+        dpre, _, db = m.moe_linear_act_grad(dy, pre, "gelu", offsets=dev, bias_grad=True)
+        return [y, pre, dpre, db, *m.moe_linear_grad(dpre, x, w, dev, dw_dtype=torch.float32)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(3):
+        x.copy_(rand((R, K), dt, 50 + i))
+        dy.copy_(rand((R, N), dt, 60 + i))
+        g.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -179,3 +179,38 @@ def test_two_streams_at_once():
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_layer_refuses_other_logits():
+    lay = layer(torch.bfloat16, 4, 2, 0, 64, 32)
+    x = rand((6, 64), torch.bfloat16, 1)
+    for bad in (rand((6, 4), torch.bfloat16, 2), rand((6, 5), torch.float32, 2), rand((5, 4), torch.float32, 2)):
+        with pytest.raises(ValueError):
+            lay.forward(x, bad)
+    with pytest.raises(ValueError):
+        lay.forward(x.half(), rand((6, 4), torch.float32, 2))
+
+
+def test_layer_on_two_streams_at_once():
+    """Two layers' passes overlap on two streams: routing scratch and all else are each call's own."""
+    dt = torch.bfloat16
+    lays = [layer(dt, 8, 2, 0, 256, 128, seed=s) for s in (0, 10)]
+    ins = [(rand((2000, 256), dt, 5 + s), rand((2000, 8), torch.float32, 7 + s), rand((2000, 256), dt, 9 + s))
+           for s in (0, 10)]
+
+    def work(i):
+        out, kept = lays[i].forward(*ins[i][:2], keep=True)
+        g = lays[i].backward(ins[i][2], kept)
+        return [out, *(g[n] for n in ("dx", "dlogits", "dw1", "dw3", "dw2"))]
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
