@@ -17,8 +17,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmilo.so")
 SOURCES = ["abi.cpp", "quant_pack.hip", "route.hip", "combine.hip", "lowrank.hip",
            "gemm_decode.hip", "gemm_prefill.hip", "gemm_prefill_128.hip", "builder.hip", "rank_policy.hip",
-           "abi_moe16.cpp", "dispatch.hip", "linear_plan.cpp", "linear_loose.hip", "linear_tile.hip", "linear_few.hip",
-           "linear_act.hip"]
+           "abi_moe16.cpp", "dispatch.hip", "linear_plan.cpp", "linear_loose.hip", "linear_packed.hip",
+           "linear_tile.hip", "linear_few.hip", "linear_act.hip"]
 # per-file flags: the 128-row tile kernels under the max-ILP scheduler
 # (measured faster there; the other kernels are neutral or spill under it)
 FILE_FLAGS = {"gemm_prefill_128.hip": ["-mllvm", "--amdgpu-sched-strategy=max-ilp"]}

@@ -185,18 +185,17 @@ int32_t milo_route_grad(const float* dslot_w, const float* logits, const int32_t
 
 size_t milo_moe_linear_workspace_bytes(const milo_linear_desc* desc) {
   if (check_linear(desc) || desc->num_rows == 0) return 0;
-  return plan_linear(kFwd, linear_args(desc)).part_bytes;
+  return plan_bytes(plan_linear(kFwd, linear_args(desc)));
 }
 
 int32_t milo_moe_linear(const milo_linear_desc* desc, void* workspace, size_t ws_bytes, void* stream) {
   set_error("%s", "");
   if (int32_t rc = check_linear(desc)) return rc;
   if (desc->num_rows == 0) return MILO_OK;
-  LinearArgs a = linear_args(desc);
+  const LinearArgs a = linear_args(desc);
   const LinearPlan p = plan_linear(kFwd, a);
-  if (int32_t rc = check_workspace(p.part_bytes, workspace, ws_bytes)) return rc;
-  a.part = (float*)workspace;
-  return launch_linear(kFwd, desc->dtype, a, p, (hipStream_t)stream);
+  if (int32_t rc = check_workspace(plan_bytes(p), workspace, ws_bytes)) return rc;
+  return launch_linear(kFwd, desc->dtype, a, p, workspace, false, (hipStream_t)stream);
 }
 
 size_t milo_moe_linear_act_grad_workspace_bytes(int32_t num_experts, int32_t N, int32_t num_rows) {
@@ -230,7 +229,7 @@ size_t milo_moe_linear_grad_workspace_bytes(const milo_linear_grad_desc* desc) {
   for (int mode = kDx; mode <= kDw; ++mode) {
     const LinearArgs a = grad_args(desc, mode);
     if (!a.out || (mode == kDx && a.rows == 0)) continue;
-    const size_t b = plan_linear(mode, a).part_bytes;
+    const size_t b = plan_bytes(plan_linear(mode, a));
     need = b > need ? b : need;
   }
   return need;
@@ -240,11 +239,13 @@ int32_t milo_moe_linear_grad(const milo_linear_grad_desc* desc, void* workspace,
   set_error("%s", "");
   if (int32_t rc = check_linear_grad(desc)) return rc;
   if (int32_t rc = check_workspace(milo_moe_linear_grad_workspace_bytes(desc), workspace, ws_bytes)) return rc;
+  bool packed = false;                                      // dy's copy, first in both products' workspace
   for (int mode = kDx; mode <= kDw; ++mode) {
-    LinearArgs a = grad_args(desc, mode);
+    const LinearArgs a = grad_args(desc, mode);
     if (!a.out || (mode == kDx && a.rows == 0)) continue;   // dw is written (zeros) without rows too
-    a.part = (float*)workspace;
-    if (int32_t rc = launch_linear(mode, desc->dtype, a, plan_linear(mode, a), (hipStream_t)stream)) return rc;
+    const LinearPlan p = plan_linear(mode, a);
+    if (int32_t rc = launch_linear(mode, desc->dtype, a, p, workspace, packed, (hipStream_t)stream)) return rc;
+    packed = p.a_bytes > 0;
   }
   return MILO_OK;
 }

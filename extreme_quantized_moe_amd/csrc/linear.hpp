@@ -27,6 +27,7 @@ struct LinearArgs {
   void* out;
   float* part;              // split contraction: partial sums
   int E, rows, N, K;
+  int lda, ldb;             // elements between rows of a and b (tile kernels)
   int max_rows;             // host bound on an expert's rows (plan only)
   int act;
   int out_f32;              // out holds float32 instead of the 16-bit type
@@ -300,13 +301,21 @@ __device__ __forceinline__ void finish_loose(const LinearArgs& a, int e, int64_t
   }
 }
 
-// 8 values at src of which `inside` are the operand's; the others read as zeros.
-__device__ __forceinline__ u32x4 load_loose(const uint16_t* src, int inside) {
-  typedef Pack<F16, 8, true> P;
-  if (inside >= 8) return __builtin_bit_cast(u32x4, *(const P*)src);
-  P p;
+// 8 values from any element on.
+__device__ __forceinline__ u32x4 load_whole(const uint16_t* src) {
+  return __builtin_bit_cast(u32x4, *(const Pack<F16, 8, true>*)src);
+}
+
+// 8 values at src, of which the row (of at least one) has `left`, perhaps none:
+// the others read as zeros.  Eight loads of two bytes without a branch, so that
+// they are in flight together; those past the end read the row's last value.
+__device__ __forceinline__ u32x4 load_cut(const uint16_t* src, int left) {
+  Pack<F16, 8, true> p;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p.v[i] = i < inside ? src[i] : (uint16_t)0;
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t v = src[i < left ? i : left - 1];
+    p.v[i] = i < left ? v : (uint16_t)0;
+  }
   return __builtin_bit_cast(u32x4, p);
 }
 
@@ -317,10 +326,15 @@ constexpr int kLinearStep = 64;   // contraction values per step of the tile ker
 struct LinearPlan {
   int kernel;          // kPlan*
   int splits;
-  int loose;           // element-aligned operands or odd row lengths
+  int loose;           // element-aligned arrays or odd row lengths: of any array, on the tile kernels of the results'
   size_t part_bytes;   // fp32 partial sums of a split contraction
+  size_t a_bytes, b_bytes;   // copies of a and b in rows of a multiple of 8 elements (0: used as they are)
 };
-enum { kPlanFew = 0, kPlanNarrow, kPlanTile128, kPlanTile256 };
+enum { kPlanFew = 0, kPlanNarrow, kPlanTile128, kPlanTile256, kPlanLoose128 };
+
+// Workspace of a plan: [copy of a][copy of b][partial sums], each part 256-byte aligned.
+inline size_t whole_lines(size_t bytes) { return (bytes + 255) / 256 * 256; }
+inline size_t plan_bytes(const LinearPlan& p) { return p.a_bytes + p.b_bytes + p.part_bytes; }
 
 constexpr int kFewWalks = 8;      // walks of 16 rows that blocks of the streaming kernel share
 
@@ -332,8 +346,12 @@ inline int few_bound(const LinearArgs& a) {
 }
 
 LinearPlan plan_linear(int mode, const LinearArgs& a);
-int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, hipStream_t st);
+// a_packed: a's copy is in the workspace already
+int32_t launch_linear(int mode, int dtype, const LinearArgs& a, const LinearPlan& p, void* workspace, bool a_packed,
+                      hipStream_t st);
 int32_t launch_linear_tile(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st);
+int32_t launch_linear_packed(int mode, int dtype, const LinearArgs& a, int kernel, hipStream_t st);
+int32_t launch_pack_rows(const void* src, int64_t rows, int len, int ld, void* dst, hipStream_t st);
 int32_t launch_linear_loose(int mode, int dtype, const LinearArgs& a, hipStream_t st);
 int32_t launch_linear_join(int mode, int dtype, const LinearArgs& a, bool loose, hipStream_t st);
 int32_t launch_linear_few(int dtype, const LinearArgs& a, bool narrow, bool loose, hipStream_t st);

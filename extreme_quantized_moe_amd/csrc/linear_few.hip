@@ -39,26 +39,31 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
   struct Piece {
     u32x4 w[NT][4], x[MT][4];
   };
+  // LOOSE: the lane's row of a group of 16, from the lane's first value on; a
+  // row past the end, whose results are not stored, reads the last one
+  const int64_t n_row0 = (int64_t)e * a.N + n0, m_row0 = base + m0;
+  auto row_of = [&](const void* p, int64_t row0, int group, int left) {
+    const int r = group + (lane & 15);
+    return (const uint16_t*)p + (row0 + (r < left ? r : left - 1)) * K + 8 * (lane >> 4);
+  };
   auto load = [&](int k0, Piece& p) {
+    if constexpr (LOOSE) {          // whole pieces only, no branch: all are in flight
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) p.w[t][s] = load_whole(row_of(a.b, n_row0, 16 * t, left_n) + k0 + 32 * s);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) p.x[t][s] = load_whole(row_of(a.a, m_row0, 16 * t, left_m) + k0 + 32 * s);
+      // all of them before the products of the piece before, not one by one
+      // where they are used
+      __builtin_amdgcn_sched_barrier(0);
+      return;
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int k = k0 + 32 * s + 8 * (lane >> 4);
-      const bool in = k < K;
-      if constexpr (LOOSE) {
-        const uint16_t* w = (const uint16_t*)a.b + ((int64_t)e * a.N + n0) * K + k;
-        const uint16_t* x = (const uint16_t*)a.a + (int64_t)(base + m0) * K + k;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int r = 16 * t + (lane & 15);
-          p.w[t][s] = load_loose(w + (int64_t)r * K, r < left_n ? K - k : 0);
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const int r = 16 * t + (lane & 15);
-          p.x[t][s] = load_loose(x + (int64_t)r * K, r < left_m ? K - k : 0);
-        }
-        continue;
-      }
+      const bool in = k0 + 32 * s + 8 * (lane >> 4) < K;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         p.w[t][s] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? at + (16 * t * K + k0 + 32 * s) * 2 : kFewOutside, 0, 0);
@@ -77,24 +82,42 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
           acc[i][j] = T::mfma(__builtin_bit_cast(s16x8, p.w[j][s]), __builtin_bit_cast(s16x8, p.x[i][s]), acc[i][j]);
   };
   constexpr int kTurn = kFewPiece * NW;
-  Piece p0, p1;
-  const int first = wave * kFewPiece;
-  load(first, p0);
-  int k = first;
-  for (; k + 2 * kTurn < K; k += 2 * kTurn) {
-    load(k + kTurn, p1);
-    use(p0);
-    load(k + 2 * kTurn, p0);
-    use(p1);
+  const int first = wave * kFewPiece, end = LOOSE ? K / kFewPiece * kFewPiece : K;
+  if (first < end) {
+    Piece p0, p1;
+    load(first, p0);
+    int k = first;
+    for (; k + 2 * kTurn < end; k += 2 * kTurn) {
+      load(k + kTurn, p1);
+      use(p0);
+      load(k + 2 * kTurn, p0);
+      use(p1);
+    }
+    // the last one or two pieces: nothing is asked for past the contraction (a
+    // load that is cut off whole still takes its turn)
+    if (k + kTurn < end) {
+      load(k + kTurn, p1);
+      use(p0);
+      use(p1);
+    } else {
+      use(p0);
+    }
   }
-  // the last one or two pieces: nothing is asked for past the contraction (a
-  // load that is cut off whole still takes its turn)
-  if (k + kTurn < K) {
-    load(k + kTurn, p1);
-    use(p0);
-    use(p1);
-  } else {
-    use(p0);
+  if (LOOSE && end < K && end / kFewPiece % NW == wave) {      // the piece that the end cuts
+#pragma unroll 1
+    for (int k = end; k < K; k += 32) {
+      s16x8 w[NT], x[MT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        w[t] = __builtin_bit_cast(s16x8, load_cut(row_of(a.b, n_row0, 16 * t, left_n) + k, K - k - 8 * (lane >> 4)));
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        x[t] = __builtin_bit_cast(s16x8, load_cut(row_of(a.a, m_row0, 16 * t, left_m) + k, K - k - 8 * (lane >> 4)));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = T::mfma(w[j], x[i], acc[i][j]);
+    }
   }
   // partial sums: lds[wave][row][16 NT columns]; lane l holds row l % 16,
   // columns 4 (l / 16) .. +3 of each product
@@ -106,16 +129,27 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, int e, int base, i
     for (int j = 0; j < NT; ++j)
       *(f32x4*)(lds + (wave * 16 * MT + 16 * i + (lane & 15)) * kLine + 16 * j + 4 * (lane >> 4)) = acc[i][j];
   __syncthreads();
+  auto sums = [&](auto first, int at) {
+    auto sum = first;
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += *(const decltype(first)*)(lds + w * 16 * MT * kLine + at);
+    return sum;
+  };
   for (int q = threadIdx.x; q < 16 * MT * 4 * NT; q += 64 * NW) {
     const int r = q / (4 * NT), c = q % (4 * NT) * 4;
-    if (m0 + r >= rows || n0 + c >= a.N) continue;
-    f32x4 sum = *(const f32x4*)(lds + r * kLine + c);
-#pragma unroll
-    for (int w = 1; w < NW; ++w) sum += *(const f32x4*)(lds + (w * 16 * MT + r) * kLine + c);
+    if (m0 + r >= rows || n0 + c + (LOOSE ? 4 : 1) > a.N) continue;
+    const f32x4 sum = sums(*(const f32x4*)(lds + r * kLine + c), r * kLine + c);
     const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    if constexpr (LOOSE) finish_loose<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, a.N - n0 - c, v);
-    else finish<T, kFwd, 4>(a, e, (int64_t)base + m0 + r, n0 + c, v);
+    finish<T, kFwd, 4, LOOSE>(a, e, (int64_t)base + m0 + r, n0 + c, v);
   }
+  // the last columns where four do not fit, one a lane
+  if (LOOSE && left_n % 4 != 0)
+    for (int q = threadIdx.x; q < 16 * MT * 4; q += 64 * NW) {
+      const int r = q / 4, c = left_n / 4 * 4 + q % 4;
+      if (m0 + r >= rows || c >= left_n) continue;
+      const float v = sums(lds[r * kLine + c], r * kLine + c);
+      finish<T, kFwd, 1, true>(a, e, (int64_t)base + m0 + r, n0 + c, &v);
+    }
 }
 
 // MT_MAX bounds the 16-row groups of one walk; an expert with fewer rows takes
@@ -141,7 +175,7 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(LinearArgs a) {
 // The same walk for few columns and many rows (a router): a block takes 16
 // rows and 64 columns, so it is x that is streamed once and w that every
 // block reads again, from the L2, which bounds it: 4096 rows of 2048 to 64
-// columns 12.5 us (x alone would take 4).
+// columns 12.7 us (x alone would take 4).
 template <class T, bool LOOSE>
 __global__ void __launch_bounds__(512) linear_narrow_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__

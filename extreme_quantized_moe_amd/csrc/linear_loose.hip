@@ -5,8 +5,11 @@
 // products of the step before run) into the same LDS layout the aligned tile
 // kernels use.  Rows past an operand's end read its last row instead, since
 // they feed results that are not stored; contraction values and columns past
-// the end read as zeros.  Bound by the loads' issue: 4096 x 14335 x 4097 over 8
-// experts forward 0.87 ms, dx 1.1, dw 1.0 (550, 435, 480 TFLOP/s).
+// the end read as zeros.  Bound by the loads: 16 bytes that start on an odd
+// element cost several aligned ones.  4096 x 14335 x 4097 over 8 experts forward
+// 0.91 ms, dx 1.05, dw 0.97 (530, 455, 495 TFLOP/s).  For few rows, where
+// copying the weights into whole rows would cost more than it saves (the plan's
+// rule).
 #include "linear_tile.hpp"
 
 namespace milo {
@@ -17,21 +20,43 @@ struct LoosePieces {
   u32x4 v[kPieces];
 
   // As Operand: deep: src is the tile's first row, `left` its rows; wide: src is
-  // the tile's first column, `left` its columns.
+  // the tile's first column, `left` its columns.  The two forms are one uniform
+  // branch a step: a branch at each load has them wait for each other (4096 x
+  // 14335 x 4097 over 8 experts dx 1302 us with one, 1054 without).
   __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int left, int depth, int k0) {
-    const bool whole = k0 + kDepth <= depth && (!WIDE || left >= 128);
+    if constexpr (!WIDE) {
+      auto rows = [&](auto piece) {
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int slot = j * 256 + threadIdx.x;
-      if constexpr (!WIDE) {
-        const int r = slot >> 3, c = k0 + (((slot & 7) ^ (r & 7)) << 3);
-        const uint16_t* row = src + (int64_t)(r < left ? r : left - 1) * ld;
-        v[j] = load_loose(row + c, whole ? 8 : depth - c);
-      } else {
-        const int k = slot >> 4, p = slot & 15;
-        const int c = ((((p >> 1) ^ Operand<true, 128, 4>::wide_swizzle(k)) << 1) | (p & 1)) << 3;
-        v[j] = load_loose(src + (int64_t)(k0 + k) * ld + c, whole ? 8 : k0 + k < depth ? left - c : 0);
-      }
+        for (int j = 0; j < kPieces; ++j) {
+          const int slot = j * 256 + threadIdx.x, r = slot >> 3;
+          v[j] = piece(src + (int64_t)(r < left ? r : left - 1) * ld, k0 + (((slot & 7) ^ (r & 7)) << 3));
+        }
+      };
+      if (k0 + kDepth <= depth) rows([&](const uint16_t* row, int k) { return load_whole(row + k); });
+      else rows([&](const uint16_t* row, int k) { return load_cut(row + k, depth - k); });
+    } else {
+      auto rows = [&](auto piece) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const int slot = j * 256 + threadIdx.x, k = slot >> 4, p = slot & 15;
+          v[j] = piece(k0 + k, ((((p >> 1) ^ Operand<true, 128, 4>::wide_swizzle(k)) << 1) | (p & 1)) << 3);
+        }
+      };
+      // Rows past the contraction read its last one and count as zeros.
+      auto rows_to_end = [&](auto piece) {
+        rows([&](int k, int c) {
+          const u32x4 some = piece(src + (k < depth ? k : depth - 1) * ld, c);
+          return k < depth ? some : u32x4{0, 0, 0, 0};
+        });
+      };
+      // Columns past the end feed results that are not stored: where another
+      // row of 8 or more follows the step, a piece may run on into it.
+      if (left >= 128 ? k0 + kDepth <= depth : k0 + kDepth < depth && ld >= 8)
+        rows([&](int k, int c) { return load_whole(src + k * ld + (c < left ? c : 0)); });
+      else if (left >= 128)
+        rows_to_end([&](const uint16_t* row, int c) { return load_whole(row + c); });
+      else
+        rows_to_end([&](const uint16_t* row, int c) { return load_cut(row + c, left - c); });
     }
   }
 
@@ -95,6 +120,7 @@ __global__ void __launch_bounds__(256, 2) linear_loose_kernel(LinearArgs a) {
     qb.store(buf + kOperand);
     __syncthreads();
     if (k + 1 < last) load(k + 1);
+    __builtin_amdgcn_sched_barrier(0);      // loads first: the products are what they wait behind
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       s16x8 xa[4], xb[4];
@@ -111,37 +137,7 @@ __global__ void __launch_bounds__(256, 2) linear_loose_kernel(LinearArgs a) {
     buf = buf == lds ? lds + kBuf : lds;
   }
   __syncthreads();
-  // Each wave turns its 64 x 64 results around in its own 16 KB (16-byte piece
-  // c of row r at place c ^ (r mod 16)), so that a lane gets 8 consecutive
-  // columns and the epilogue's code is there once.
-  char* mine = lds + wave * 16384;
-  const int r0 = lane & 15;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *(f32x4*)(mine + (16 * i + r0) * 256 + (((4 * j + (lane >> 4)) ^ r0) << 4)) = acc[i][j];
-  const int n = n0 + wn + 8 * (lane & 7);
-#pragma unroll 1
-  for (int it = 0; it < 8; ++it) {
-    const int r = 8 * it + (lane >> 3), m = m0 + wm + r, p = 2 * (lane & 7);
-    const f32x4 lo = *(const f32x4*)(mine + r * 256 + ((p ^ (r & 15)) << 4));
-    const f32x4 hi = *(const f32x4*)(mine + r * 256 + (((p + 1) ^ (r & 15)) << 4));
-    if (m >= M || n >= cols) continue;
-    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    const int64_t row = (MODE == kDw ? 0 : s.span.base) + (int64_t)m;
-    if (a.splits > 1) {
-      LinearArgs part = a;                   // this split's sums as they are
-      part.out = a.part + (int64_t)split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols;
-      part.out_f32 = 1;
-      part.act = MILO_ACT_NONE;
-      part.bias = part.mul = part.residual = nullptr;
-      part.pre = nullptr;
-      finish_loose<T, MODE, 8>(part, s.e, row, n, cols - n, v);
-    } else {
-      finish_loose<T, MODE, 8>(a, s.e, row, n, cols - n, v);
-    }
-  }
+  finish_turned<T, MODE>(a, s.e, MODE == kDw ? 0 : s.span.base, M, m0 + wm, n0 + wn, split, lds + wave * kTurned, acc);
 #endif
 }
 

@@ -3,28 +3,6 @@
 
 namespace milo {
 
-template <class T, int MODE, int ACT, int BM, int BN, int WM, int WN>
-static hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
-  const int64_t tn = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
-  const int64_t rows = MODE == kDw ? (int64_t)a.E * ((a.N + BM - 1) / BM)
-                                   : (a.rows + BM - 1) / BM + (a.E > 1 ? a.E : 0);
-  // as many blocks as run at once (one or two to a compute unit: the LDS
-  // ring), a multiple of 8 so that a block's tiles stay on its XCD
-  const int64_t slots = (int64_t)device_cu_count() * (BM == 256 ? 1 : 2);
-  int64_t blocks = rows * tn * a.splits;
-  blocks = (blocks < slots ? blocks + 7 : slots) / 8 * 8;
-  if (blocks < 8) blocks = 8;
-  constexpr size_t bytes = tile_lds<BM, BN>();
-  const void* fn = (const void*)linear_tile_kernel<T, MODE, ACT, BM, BN, WM, WN>;
-  if (bytes + sizeof(ExpertTable) > 65536) {
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((linear_tile_kernel<T, MODE, ACT, BM, BN, WM, WN>), dim3((unsigned)blocks), dim3(64 * WM * WN),
-                     bytes, st, a);
-  return hipGetLastError();
-}
-
 template <class T, int MODE, int ACT>
 static hipError_t run_mode(const LinearArgs& a, int kernel, hipStream_t st) {
   return kernel == kPlanTile256 ? run_tile<T, MODE, ACT, 256, 256, 2, 4>(a, st)
@@ -68,16 +46,17 @@ __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a) {
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < a.splits; ++s) {
     const float* p = a.part + s * one + at;
-    if constexpr (LOOSE) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += n + c < cols ? p[c] : 0.f;
-    } else {
-      const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 4);
+    if (!LOOSE || n + 8 <= cols) {
+      typedef Pack<F32, 4, LOOSE> Four;
+      const Four lo = *(const Four*)p, hi = *(const Four*)(p + 4);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        v[c] += lo[c];
-        v[4 + c] += hi[c];
+        v[c] += lo.v[c];
+        v[4 + c] += hi.v[c];
       }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += n + c < cols ? p[c] : 0.f;
     }
   }
   if constexpr (LOOSE) finish_loose<T, MODE, 8>(a, e, row, n, cols - n, v);

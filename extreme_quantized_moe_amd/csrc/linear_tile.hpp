@@ -1,6 +1,7 @@
 // The grouped 16-bit product on the matrix cores: BM x BN output tiles, the
-// contraction in steps of 64 through LDS.  Needs row lengths of a multiple of
-// 8 elements and 16-byte aligned operands (the plan's rule); any row count.
+// contraction in steps of 64 through LDS.  Needs operands whose rows start on
+// 16-byte addresses (the plan's rule); any row count, and with LOOSE results of
+// any row length and alignment.
 //
 // Bound by the matrix cores where the contraction is long.  256 x 256 tiles,
 // eight waves of 128 x 64 (128 accumulator registers, two waves a SIMD, two
@@ -316,6 +317,50 @@ __device__ __forceinline__ u32x4 rounded(const float* v) {
   return __builtin_bit_cast(u32x4, o);
 }
 
+// Results of a wave for arrays of any alignment and row length: 64 rows x 64
+// columns from row m, column n on, turned around in the wave's own LDS (16-byte
+// piece c of row r at place c ^ (r mod 16)), so that a lane gets 8 consecutive
+// columns and the epilogue's code is there once.
+constexpr int kTurned = 64 * 64 * 4;
+template <class T, int MODE>
+__device__ __forceinline__ void finish_turned(const LinearArgs& a, int e, int base, int M, int m0, int n0, int split,
+                                              char* mine, const f32x4 (*acc)[4]) {
+  const int lane = threadIdx.x & 63, r0 = lane & 15, cols = MODE == kFwd ? a.N : a.K;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *(f32x4*)(mine + (16 * i + r0) * 256 + (((4 * j + (lane >> 4)) ^ r0) << 4)) = acc[i][j];
+  LinearArgs to = a;
+  if (a.splits > 1) {                      // this split's sums as they are
+    to.out = a.part + (int64_t)split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols;
+    to.out_f32 = 1;
+    to.act = MILO_ACT_NONE;
+    to.bias = to.mul = to.residual = nullptr;
+    to.pre = nullptr;
+  }
+  const int n = n0 + 8 * (lane & 7);
+#pragma unroll 1
+  for (int it = 0; it < 8; ++it) {
+    const int r = 8 * it + (lane >> 3), p = 2 * (lane & 7);
+    const f32x4 lo = *(const f32x4*)(mine + r * 256 + ((p ^ (r & 15)) << 4));
+    const f32x4 hi = *(const f32x4*)(mine + r * 256 + (((p + 1) ^ (r & 15)) << 4));
+    if (m0 + r >= M || n + 8 > cols) continue;
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    finish<T, MODE, 8, true>(to, e, base + (int64_t)(m0 + r), n, v);
+  }
+  // The piece that the last column cuts, a column at a time over all 64 rows
+  // (within the loop above, piece by piece, it made the last column tile
+  // 40 us longer).
+  const int left = cols - n0;
+  if (left > 0 && left < 64 && m0 + lane < M)
+#pragma unroll 1
+    for (int c = left & ~7; c < left; ++c) {
+      const float v = *(const float*)(mine + lane * 256 + (((c >> 2) ^ r0) << 4) + (c & 3) * 4);
+      finish<T, MODE, 1, true>(to, e, base + (int64_t)(m0 + lane), n0 + c, &v);
+    }
+}
+
 constexpr int kAhead = 2;   // row groups whose epilogue operands are asked for at a time
 
 // Persistent blocks: block b takes tiles b, b + grid, ...  The steps of all its
@@ -330,8 +375,9 @@ constexpr int kAhead = 2;   // row groups whose epilogue operands are asked for 
 // the step after has arrived.
 //
 // ACT: the activation of a forward launch (MILO_ACT_NONE also stands for
-// RELU), a template so that each kernel holds one activation's code.
-template <class T, int MODE, int ACT, int BM, int BN, int WM, int WN>
+// RELU), a template so that each kernel holds one activation's code.  LOOSE:
+// the stream of loads stops at each tile's end, its results go through LDS.
+template <class T, int MODE, int ACT, int BM, int BN, int WM, int WN, bool LOOSE = false>
 __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass has no gfx950 builtins; it needs the launch stub only
   constexpr int NW = WM * WN, NI = BM / WM / 16, NJ = BN / WN / 16;
@@ -343,7 +389,7 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   constexpr int kBuf = OpA::kBytes + OpB::kBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = MODE == kFwd ? a.N : a.K;
-  const int64_t lda = MODE == kFwd ? a.K : a.N, ldb = a.K;
+  const int64_t lda = a.lda, ldb = a.ldb;
 
   if (wave == 0) {
     int before[2] = {0, 0};
@@ -393,10 +439,11 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
     }
     step = ahead.first;
     pa = (const uint16_t*)a.a + (int64_t)ahead.base * lda + (AW ? (int64_t)ahead.m0 : ahead.m0 * lda);
-    pb = (const uint16_t*)a.b + (MODE == kDw ? (int64_t)ahead.base * ldb : (int64_t)ahead.e * a.N * a.K) +
+    pb = (const uint16_t*)a.b + (MODE == kDw ? (int64_t)ahead.base * ldb : (int64_t)ahead.e * a.N * ldb) +
          (BW ? (int64_t)ahead.n0 : ahead.n0 * ldb);
-    lefta = AW || ahead.M - ahead.m0 < BM ? ahead.M - ahead.m0 : BM;
-    leftb = BW || cols - ahead.n0 < BN ? cols - ahead.n0 : BN;
+    // wide: to the end of the row's last piece of 8 (rows are padded to whole pieces)
+    lefta = AW ? (ahead.M - ahead.m0 + 7) & ~7 : ahead.M - ahead.m0 < BM ? ahead.M - ahead.m0 : BM;
+    leftb = BW ? (cols - ahead.n0 + 7) & ~7 : cols - ahead.n0 < BN ? cols - ahead.n0 : BN;
     oa.init(lane, wave, (int)lda, ahead.M - ahead.m0);
     ob.init(lane, wave, (int)ldb, cols - ahead.n0);
   };
@@ -407,7 +454,7 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
     ob.load(pb, ldb, leftb, ahead.D, step * kDepth, on, dst + OpA::kBytes, wave);
   };
   auto advance = [&]() {
-    if (++step >= ahead.last && ahead.e >= 0) {
+    if (++step >= ahead.last && ahead.e >= 0 && !LOOSE) {
       ahead_id += gridDim.x;
       seek();
     }
@@ -415,12 +462,15 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   oa.init(lane, wave, (int)lda, 0);
   ob.init(lane, wave, (int)ldb, 0);
   ahead.e = -1;
-  seek();
-  issue(0);
-  advance();
-  issue(1);
-  advance();
-  arrived();
+  auto start = [&]() {
+    seek();
+    issue(0);
+    advance();
+    issue(1);
+    advance();
+    arrived();
+  };
+  if constexpr (!LOOSE) start();
 
   // ---- one tile with NIX of the NI row groups of a wave
   const int wn = wave % WN * (BN / WN);
@@ -467,6 +517,18 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
       }
     }
 
+    if constexpr (LOOSE) {
+      // The stream has stopped behind this tile, so that the LDS is free for
+      // the results; it starts again at the block's next tile.
+      static_assert(NJ == 4 && NIX % 4 == 0 && NW * kTurned <= 2 * kBuf, "64 x 64 results a wave at a time");
+      arrived();
+#pragma unroll
+      for (int g = 0; g < NIX; g += 4)
+        finish_turned<T, MODE>(a, t.e, (MODE == kDw ? 0 : t.base), t.M, t.m0 + wm + 16 * g, t.n0 + wn, t.split,
+                               lds + wave * kTurned, &acc[g]);
+      __syncthreads();
+      return;
+    }
     // ---- results.  Lane l holds row l % 16, columns 4 (l / 16) .. +3 of each
     // 16 x 16 product.  All accesses go through buffer resources that begin at
     // the tile and end with its last row, columns past the end get an offset
@@ -571,6 +633,11 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   for (int id = blockIdx.x;; id += gridDim.x) {   // find_tile may move id on
     const Tile t = find_tile<MODE, BM, BN>(a, tab, id);
     if (t.e < 0) break;
+    if constexpr (LOOSE) {
+      ahead_id = id;
+      buf = 0;
+      start();
+    }
     if constexpr (NI == 8) {
       if (t.M - t.m0 <= BM / 2) {
         tile(t, std::integral_constant<int, NI / 2>());
@@ -582,6 +649,28 @@ __global__ void __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) linear_tile_k
   // the loads past the last step (of nothing) have ended before the LDS is given back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #endif
+}
+
+template <class T, int MODE, int ACT, int BM, int BN, int WM, int WN, bool LOOSE = false>
+static hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
+  const int64_t tn = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
+  const int64_t rows = MODE == kDw ? (int64_t)a.E * ((a.N + BM - 1) / BM)
+                                   : (a.rows + BM - 1) / BM + (a.E > 1 ? a.E : 0);
+  // as many blocks as run at once (one or two to a compute unit: the LDS
+  // ring), a multiple of 8 so that a block's tiles stay on its XCD
+  const int64_t slots = (int64_t)device_cu_count() * (BM == 256 ? 1 : 2);
+  int64_t blocks = rows * tn * a.splits;
+  blocks = (blocks < slots ? blocks + 7 : slots) / 8 * 8;
+  if (blocks < 8) blocks = 8;
+  constexpr size_t bytes = tile_lds<BM, BN>();
+  const void* fn = (const void*)linear_tile_kernel<T, MODE, ACT, BM, BN, WM, WN, LOOSE>;
+  if (bytes + sizeof(ExpertTable) > 65536) {
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((linear_tile_kernel<T, MODE, ACT, BM, BN, WM, WN, LOOSE>), dim3((unsigned)blocks),
+                     dim3(64 * WM * WN), bytes, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace milo

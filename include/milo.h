@@ -591,7 +591,8 @@ int32_t milo_route_grad(const float* dslot_w, const float* logits, const int32_t
  *             only the choice of kernels depends on it, never a result's
  *             correctness.
  * workspace : milo_moe_linear_workspace_bytes(desc) bytes (may be 0), 256-byte
- *             aligned, scratch only.  Calls that overlap in time need
+ *             aligned, scratch only; the size is that of this desc, its
+ *             pointers' alignment included.  Calls that overlap in time need
  *             workspaces of their own.
  * Capturable into a HIP graph.  Constraints: 1 <= num_experts <= 256,
  * 1 <= N, K <= 65536, 0 <= num_rows <= 2^20, all pointers aligned to their element (16 bytes, with N
