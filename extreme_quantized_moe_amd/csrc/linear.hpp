@@ -284,23 +284,6 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int e, int64_t row, 
   store_out<T, V, LOOSE>(a, at, v);
 }
 
-// V columns of one row, of which `left` are inside: whole, or one by one.
-template <class T, int MODE, int V>
-__device__ __forceinline__ void finish_loose(const LinearArgs& a, int e, int64_t row, int col, int left,
-                                             const float* v) {
-  if (left >= V) {
-    finish<T, MODE, V, true>(a, e, row, col, v);
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < left; ++i) {
-      float one = v[0];
-#pragma unroll
-      for (int c = 1; c < V; ++c) one = i == c ? v[c] : one;   // a runtime index would put v in memory
-      finish<T, MODE, 1, true>(a, e, row, col + i, &one);
-    }
-  }
-}
-
 // 8 values from any element on.
 __device__ __forceinline__ u32x4 load_whole(const uint16_t* src) {
   return __builtin_bit_cast(u32x4, *(const Pack<F16, 8, true>*)src);

@@ -41,26 +41,29 @@ __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a) {
     e = s.e;
     row = s.span.base + (int64_t)s.local * 4 + wave;
   }
-  if (n >= cols) return;
-  const int64_t one = (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols, at = out_at<MODE>(a, e, row, n);
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float* p = a.part + s * one + at;
-    if (!LOOSE || n + 8 <= cols) {
+  const int64_t one = (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols;
+  if (n + (LOOSE ? 8 : 1) <= cols) {
+    const int64_t at = out_at<MODE>(a, e, row, n);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.splits; ++s) {
       typedef Pack<F32, 4, LOOSE> Four;
+      const float* p = a.part + s * one + at;
       const Four lo = *(const Four*)p, hi = *(const Four*)(p + 4);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         v[c] += lo.v[c];
         v[4 + c] += hi.v[c];
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += n + c < cols ? p[c] : 0.f;
     }
+    finish<T, MODE, 8, LOOSE>(a, e, row, n, v);
   }
-  if constexpr (LOOSE) finish_loose<T, MODE, 8>(a, e, row, n, cols - n, v);
-  else finish<T, MODE, 8>(a, e, row, n, v);
+  // the last columns where eight do not fit, one a lane
+  if (LOOSE && blockIdx.y == gridDim.y - 1 && (int)(threadIdx.x & 63) < cols % 8) {
+    const int c = cols / 8 * 8 + (threadIdx.x & 63);
+    float v = 0.f;
+    for (int s = 0; s < a.splits; ++s) v += a.part[s * one + out_at<MODE>(a, e, row, c)];
+    finish<T, MODE, 1, true>(a, e, row, c, &v);
+  }
 }
 
 template <class T, int MODE>
