@@ -1,5 +1,8 @@
 // The storage types of the 16-bit (and 32-bit) MoE operators: conversion to
-// float, rounding back (nearest even), and one 8-wide matrix-core operand.
+// float, rounding back (nearest even), and one 8-wide matrix-core operand; and
+// what the host code of these operators shares.  (Not in milo_internal.hpp: the
+// committed traffic measurement of the int3 decode kernel holds for one state
+// of the files which that kernel is built from.)
 #pragma once
 
 #include "milo_internal.hpp"
@@ -51,5 +54,17 @@ inline int access_bytes(size_t row_bytes, const void* a, const void* b = nullptr
   const uintptr_t bits = (uintptr_t)row_bytes | (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)d;
   return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
 }
+
+int device_cu_count();   // compute units of the current device (abi.cpp)
+
+// rows to the experts and back (dispatch.hip)
+int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
+                       void* y, hipStream_t st);
+int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int64_t tokens, int slots, int H,
+                         int64_t rows, int dtype, void* out, hipStream_t st);
+int32_t launch_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
+                              int slots, int H, int64_t rows, int dtype, void* dy, float* dw, hipStream_t st);
+int32_t launch_route_grad(const float* dslot_w, const float* logits, const int32_t* ids, int64_t tokens, int E, int k,
+                          int S, int renorm, float* dlogits, hipStream_t st);
 
 }  // namespace milo

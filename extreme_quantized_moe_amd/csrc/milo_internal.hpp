@@ -217,7 +217,6 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ offset
 // ---------------------------------------------------------------- host side
 void set_error(const char* fmt, ...);
 int32_t hip_status(hipError_t e, const char* what);
-int device_cu_count();   // compute units of the current device
 
 // launchers (return MILO_OK or MILO_ERR_HIP)
 int32_t launch_quantize(const float* W, int64_t rows, int64_t K, int group, uint8_t* codes,
@@ -234,16 +233,6 @@ int32_t launch_route(const float* logits, int T, int E, int k, int S, int renorm
                      int32_t* ids, float* w, float* slot_w, int32_t* sorted_pairs,
                      int32_t* pair_pos, int32_t* offsets, void* ws, hipStream_t st);
 int32_t launch_combine(const float* y, int T, int slots, int H, uint16_t* out, hipStream_t st);
-
-// rows to the experts and back (dispatch.hip)
-int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
-                       void* y, hipStream_t st);
-int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int64_t tokens, int slots, int H,
-                         int64_t rows, int dtype, void* out, hipStream_t st);
-int32_t launch_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
-                              int slots, int H, int64_t rows, int dtype, void* dy, float* dw, hipStream_t st);
-int32_t launch_route_grad(const float* dslot_w, const float* logits, const int32_t* ids, int64_t tokens, int E, int k,
-                          int S, int renorm, float* dlogits, hipStream_t st);
 
 // compensator construction (builder.hip)
 size_t svd_workspace_bytes(int64_t N, int64_t K, int l);
