@@ -2,6 +2,7 @@
 without the `milo_` prefix).  torch supplies device memory and the current
 stream; every computation runs in the library's HIP kernels.  There is no
 fallback: if libmilo.so is missing, importing the binding raises."""
+import contextlib
 import ctypes as C
 
 import torch
@@ -14,6 +15,11 @@ _DEV_CHECKED = set()
 
 def _stream():
     return torch.cuda.current_stream().cuda_stream
+
+
+def _on(dev):
+    """Context with `dev` as the current device."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _p(t):
@@ -199,8 +205,9 @@ _route_ws = {}
 def route_sort(logits, k, S=0, renormalize=True, own_scratch=False):
     """Softmax top-k routing + expert sort.  Returns dict of device tensors:
     ids [T][k], w [T][k], slot_w [T*(k+S)], sorted_pairs, pair_pos [T*(k+S)],
-    offsets [E+S+1].  own_scratch: scratch of this call's own instead of the
-    device's kept one (calls that overlap: several streams or graphs)."""
+    offsets [E+S+1].  Runs on the logits' device, on its current stream.
+    own_scratch: scratch of this call's own instead of the device's kept one
+    (calls that overlap: several streams or graphs)."""
     logits = logits.contiguous()
     _cuda(logits)
     T, E = logits.shape
@@ -224,10 +231,11 @@ def route_sort(logits, k, S=0, renormalize=True, own_scratch=False):
         if ws is None:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             _route_ws[key] = ws
-    check("milo_route_sort", L.lib().milo_route_sort(
-        _p(logits), T, E, k, S, 1 if renormalize else 0, _p(out["ids"]), _p(out["w"]),
-        _p(out["slot_w"]), _p(out["sorted_pairs"]), _p(out["pair_pos"]), _p(out["offsets"]),
-        _p(ws), nbytes, _stream()))
+    with _on(dev):
+        check("milo_route_sort", L.lib().milo_route_sort(
+            _p(logits), T, E, k, S, 1 if renormalize else 0, _p(out["ids"]), _p(out["w"]),
+            _p(out["slot_w"]), _p(out["sorted_pairs"]), _p(out["pair_pos"]), _p(out["offsets"]),
+            _p(ws), nbytes, _stream()))
     return out
 
 
