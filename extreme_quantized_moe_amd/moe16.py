@@ -45,18 +45,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _run(name, dev, *args):
-    """Calls milo_<name>(*args, stream) on the device's current stream, with
-    the device current.  (torch.cuda.current_stream builds a Stream object for
-    this; a decoding step's calls take a few microseconds in all.)"""
-    index = dev.index
+def _call(name, dev, *args):
+    """The library's `name` with `dev` as the current device: launches go there,
+    and plans (so workspace sizes too) take its number of compute units."""
     fn = getattr(L.lib(), name)
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+    if torch._C._cuda_getDevice() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _run(name, dev, *args):
+    """Calls the library's `name` with (*args, stream) on the device's current
+    stream.  (torch.cuda.current_stream builds a Stream object for this; a
+    decoding step's calls take a few microseconds in all.)"""
+    rc = _call(name, dev, *args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc:
         check(name, rc)
 
@@ -231,7 +234,7 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
     ref = C.byref(L.MiloLinearDesc(
         E, N, K, R, max_rows_per_expert, code, L.F32 if odt is torch.float32 else code, _act(activation), x.data_ptr(),
         w.data_ptr(), _ptr(offsets), _ptr(bias), _ptr(mul), _ptr(residual), _ptr(pre), out.data_ptr()))
-    nbytes = L.lib().milo_moe_linear_workspace_bytes(ref)
+    nbytes = _call("milo_moe_linear_workspace_bytes", dev, ref)
     ws = _scratch(nbytes, dev)
     _run("milo_moe_linear", dev, ref, _ptr(ws), nbytes)
     return (out, pre) if return_pre else out
@@ -288,7 +291,7 @@ def moe_linear_grad(dy, x, w, offsets=None, need_dx=True, need_dw=True, dw_dtype
     ref = C.byref(L.MiloLinearGradDesc(
         E, N, K, R, code, L.F32 if odt is torch.float32 else code, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
         _ptr(offsets), _ptr(dx_add), _ptr(dx), _ptr(dw)))
-    nbytes = L.lib().milo_moe_linear_grad_workspace_bytes(ref)
+    nbytes = _call("milo_moe_linear_grad_workspace_bytes", dev, ref)
     ws = _scratch(nbytes, dev)
     _run("milo_moe_linear_grad", dev, ref, _ptr(ws), nbytes)
     return dx, dw

@@ -77,3 +77,25 @@ def ran_on(calls, name):
 def test_routing_runs_on_the_logits_device(calls):
     m.route_sort(Tensor(torch.float32, 6, 4), 2, own_scratch=True)
     assert ran_on(calls, "milo_route_sort") == {(1, 701)}
+
+
+def test_workspaces_are_sized_for_the_tensors_device(calls):
+    dt = torch.bfloat16
+    x, w, dy = Tensor(dt, 40, 64), Tensor(dt, 32, 64), Tensor(dt, 40, 32)
+    m.moe_linear(x, w)
+    m.moe_linear_grad(dy, x, w)
+    for name in ("milo_moe_linear", "milo_moe_linear_grad"):
+        assert ran_on(calls, name) == {(1, 701)}
+        assert {dev for dev, _ in ran_on(calls, name + "_workspace_bytes")} == {1}
+
+
+def test_layer_runs_on_its_own_device(calls, monkeypatch):
+    """Every call of a layer whose weights and inputs are on device 1."""
+    dt = torch.float16
+    monkeypatch.setattr(torch, "zeros", torch.empty)
+    monkeypatch.setattr(torch, "empty_like", lambda t: Tensor(t.dtype, *t.shape))
+    layer = m.MoELayer16(Tensor(dt, 4, 32, 64), Tensor(dt, 4, 32, 64), Tensor(dt, 4, 64, 32), 4, 2)
+    _, kept = layer.forward(Tensor(dt, 6, 64), Tensor(torch.float32, 6, 4), keep=True)
+    layer.backward(Tensor(dt, 6, 64), kept)
+    on = {(n, dev) for n, dev, _ in calls if n not in ("milo_route_workspace_bytes",)}
+    assert len(on) >= 10 and {dev for _, dev in on} == {1}, on
