@@ -288,11 +288,23 @@ static void run_unpermute_grad(const void* dout, const void* y, const int32_t* p
 
 static size_t elem_bytes(int dtype) { return dtype == MILO_F32 ? 4 : 2; }
 
+// Tokens of one launch: it takes fewer than 2^32 threads, and a token up to
+// 256.  (unpermute_grad takes 64 a token from 2048 on.)
+constexpr int64_t kMostTokens = 1 << 23;
+
+// run(first token, tokens) for every launch's share.
+template <class Run>
+static void by_launches(int64_t tokens, Run run) {
+  for (int64_t t = 0; t < tokens; t += kMostTokens) run(t, tokens - t < kMostTokens ? tokens - t : kMostTokens);
+}
+
 int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
                        void* y, hipStream_t st) {
   const int bytes = access_bytes(H * elem_bytes(dtype), x, y);
 #define RUN(T, V, ...) run_permute<T, V>(__VA_ARGS__)
-  MILO_BY_TYPE(RUN, x, pos, tokens, slots, H, rows, y, st);
+  by_launches(tokens, [&](int64_t t, int64_t n) {
+    MILO_BY_TYPE(RUN, (const char*)x + t * H * elem_bytes(dtype), pos + t * slots, n, slots, H, rows, y, st);
+  });
 #undef RUN
   return hip_status(hipGetLastError(), "permute_kernel launch");
 }
@@ -305,7 +317,10 @@ int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int6
     if (w) run_unpermute<T, V, true>(__VA_ARGS__); \
     else run_unpermute<T, V, false>(__VA_ARGS__);  \
   } while (0)
-  MILO_BY_TYPE(RUN, y, pos, w, tokens, slots, H, rows, out, st);
+  by_launches(tokens, [&](int64_t t, int64_t n) {
+    MILO_BY_TYPE(RUN, y, pos + t * slots, w ? w + t * slots : w, n, slots, H, rows,
+                 (char*)out + t * H * elem_bytes(dtype), st);
+  });
 #undef RUN
   return hip_status(hipGetLastError(), "unpermute_kernel launch");
 }
