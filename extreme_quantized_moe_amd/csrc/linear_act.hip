@@ -24,14 +24,15 @@ __device__ __forceinline__ void act_grad_piece(int act, const Pack<T, V>& g, con
   }
 }
 
+// In both kernels dpre and dmul may be the buffers of dy, pre or mul, so none of
+// the five is `restrict`: a thread reads all it needs of an element before it
+// writes there, and no other thread touches that element.
+
 // ---- without bias gradients the experts' rows are one flat run of elements
 template <class T, int V, bool MUL>
-__global__ void __launch_bounds__(256) act_grad_kernel(const uint16_t* __restrict__ dy,
-                                                       const uint16_t* __restrict__ pre,
-                                                       const uint16_t* __restrict__ mul,
+__global__ void __launch_bounds__(256) act_grad_kernel(const uint16_t* dy, const uint16_t* pre, const uint16_t* mul,
                                                        const int32_t* __restrict__ offsets, int E, int N, int rows,
-                                                       int act, uint16_t* __restrict__ dpre,
-                                                       uint16_t* __restrict__ dmul) {
+                                                       int act, uint16_t* dpre, uint16_t* dmul) {
   typedef Pack<T, V> P;
   const Span s = offsets ? clip_span(offsets[0], offsets[E], rows) : Span{0, rows};
   const int64_t first = (int64_t)s.base * N / V, count = (int64_t)s.rows * N / V;   // V divides N
@@ -48,16 +49,16 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const uint16_t* __restric
 
 // ---- with bias gradients a block takes kActRows rows of one expert: its
 // threads are 2^lg column pieces by 256 / 2^lg rows, each sums its rows in
-// order, and the row groups are joined in LDS in order: part[tile][N].
-constexpr int kActRows = 32;
+// order, and the row groups are joined in LDS in order: part[tile][N].  A thread
+// asks for kActTurns of its rows at a time, before it writes any of them.
+constexpr int kActRows = 32, kActTurns = 4;
 
 template <class T, int V, bool MUL>
-__global__ void __launch_bounds__(256) act_grad_bias_kernel(const uint16_t* __restrict__ dy,
-                                                            const uint16_t* __restrict__ pre,
-                                                            const uint16_t* __restrict__ mul,
+__global__ void __launch_bounds__(256) act_grad_bias_kernel(const uint16_t* dy, const uint16_t* pre,
+                                                            const uint16_t* mul,
                                                             const int32_t* __restrict__ offsets, int E, int N,
-                                                            int rows, int act, int lg, uint16_t* __restrict__ dpre,
-                                                            uint16_t* __restrict__ dmul, float* __restrict__ part) {
+                                                            int rows, int act, int lg, uint16_t* dpre,
+                                                            uint16_t* dmul, float* __restrict__ part) {
   typedef Pack<T, V> P;
   __shared__ float sums[256 * V];
   const int id = blockIdx.y;
@@ -71,18 +72,27 @@ __global__ void __launch_bounds__(256) act_grad_bias_kernel(const uint16_t* __re
 #pragma unroll
   for (int i = 0; i < V; ++i) total[i] = 0.f;
   if (c < pieces)
-#pragma unroll 4
-    for (int r = r0 + rg; r < r1; r += down) {
-      const int64_t at = (int64_t)(s.span.base + r) * pieces + c;
-      const P g = ((const P*)dy)[at], p = ((const P*)pre)[at];
-      P m = g, o, om;
-      if (MUL) m = ((const P*)mul)[at];
-      float d[V];
-      act_grad_piece<T, V, MUL>(act, g, p, m, d, &o, &om);
-      ((P*)dpre)[at] = o;
-      if (MUL) ((P*)dmul)[at] = om;
+    for (int r = r0 + rg; r < r1; r += kActTurns * down) {
+      P g[kActTurns], p[kActTurns], m[kActTurns];
+      const int64_t first = (int64_t)(s.span.base + r) * pieces + c, step = (int64_t)down * pieces;
 #pragma unroll
-      for (int i = 0; i < V; ++i) total[i] += d[i];
+      for (int t = 0; t < kActTurns; ++t) {
+        const int64_t at = first + (r + t * down < r1 ? t : 0) * step;   // past the last row: this one again
+        g[t] = ((const P*)dy)[at];
+        p[t] = ((const P*)pre)[at];
+        m[t] = MUL ? ((const P*)mul)[at] : g[t];
+      }
+#pragma unroll
+      for (int t = 0; t < kActTurns; ++t) {
+        if (r + t * down >= r1) break;
+        float d[V];
+        P o, om;
+        act_grad_piece<T, V, MUL>(act, g[t], p[t], m[t], d, &o, &om);
+        ((P*)dpre)[first + t * step] = o;
+        if (MUL) ((P*)dmul)[first + t * step] = om;
+#pragma unroll
+        for (int i = 0; i < V; ++i) total[i] += d[i];
+      }
     }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[threadIdx.x * V + i] = total[i];
