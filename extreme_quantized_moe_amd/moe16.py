@@ -41,11 +41,11 @@ def _float_type(name, t, wide=True):
     return code
 
 
-def _fit(*sizes):
-    """Refuses sizes that the library's 32-bit numbers do not hold: ctypes
-    would pass them on modulo 2^32, as another and allowed size."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError(f"a size of {max(sizes)} does not fit a 32-bit number")
+def _too_large(*sizes):
+    """The library's sizes are 32-bit numbers, and ctypes would pass larger
+    ones on modulo 2^32, as others that are allowed.  Callers test
+    (a | b | ...) >> 31: true for a size outside 0 .. 2^31 - 1."""
+    raise ValueError(f"a size does not fit a 32-bit number: {', '.join(map(str, sizes))}")
 
 
 def _ptr(t):
@@ -66,7 +66,12 @@ def _run(name, dev, *args):
     """Calls the library's `name` with (*args, stream) on the device's current
     stream.  (torch.cuda.current_stream builds a Stream object for this; a
     decoding step's calls take a few microseconds in all.)"""
-    rc = _call(name, dev, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        rc = getattr(L.lib(), name)(*args, stream)
+    else:
+        rc = _call(name, dev, *args, stream)
     if rc:
         check(name, rc)
 
@@ -81,7 +86,8 @@ def _scratch(nbytes, dev):
 
 def _pairs(pair_pos, slots, dev):
     n = pair_pos.numel()
-    _fit(n)
+    if n >> 31:
+        _too_large(n)
     _need(slots >= 1 and n % slots == 0, f"pair_pos holds {n} entries, not a multiple of {slots} slots")
     _tensor("pair_pos", pair_pos, torch.int32, pair_pos.shape, dev)
     return n // slots
@@ -89,7 +95,8 @@ def _pairs(pair_pos, slots, dev):
 
 def _rows_out(num_rows, H, pairs, like, dropped):
     """An expert-ordered output: zeros where rows may stay without a pair."""
-    _fit(num_rows)
+    if num_rows >> 31:
+        _too_large(num_rows)
     new = torch.zeros if dropped or num_rows > pairs else torch.empty
     return new((num_rows, H), dtype=like.dtype, device=like.device)
 
@@ -105,7 +112,8 @@ def moe_permute(x, pair_pos, slots, num_rows=None, dropped=False, out=None):
     _need(x.dim() == 2, "x must be [T][H]")
     dev = x.device
     T, H = x.shape
-    _fit(T, H, slots)
+    if (T | H | slots) >> 31:
+        _too_large(T, H, slots)
     _tensor("x", x, x.dtype, x.shape)
     _need(_pairs(pair_pos, slots, dev) == T, f"pair_pos must hold {T} x {slots} entries")
     if out is None:
@@ -113,7 +121,8 @@ def moe_permute(x, pair_pos, slots, num_rows=None, dropped=False, out=None):
         out = _rows_out(num_rows, H, T * slots, x, dropped)
     else:
         num_rows = out.shape[0] if num_rows is None else num_rows
-        _fit(num_rows)
+        if num_rows >> 31:
+            _too_large(num_rows)
         _tensor("out", out, x.dtype, (num_rows, H), dev)
     _run("milo_moe_permute", dev, x.data_ptr(), pair_pos.data_ptr(), T, slots, H, num_rows, code, out.data_ptr())
     return out
@@ -134,7 +143,8 @@ def moe_unpermute(y, pair_pos, slots, slot_w=None, out=None):
     _need(y.dim() == 2, "y must be [num_rows][H]")
     dev = y.device
     R, H = y.shape
-    _fit(R, H, slots)
+    if (R | H | slots) >> 31:
+        _too_large(R, H, slots)
     _tensor("y", y, y.dtype, y.shape)
     T = _pairs(pair_pos, slots, dev)
     if slot_w is not None:
@@ -158,7 +168,8 @@ def moe_unpermute_grad(dout, y, pair_pos, slots, slot_w=None, dropped=False, out
     dev = dout.device
     T, H = dout.shape
     R = y.shape[0]
-    _fit(T, H, R, slots)
+    if (T | H | R | slots) >> 31:
+        _too_large(T, H, R, slots)
     _tensor("dout", dout, dout.dtype, dout.shape)
     _tensor("y", y, dout.dtype, (R, H), dev)
     _need(_pairs(pair_pos, slots, dev) == T, f"pair_pos must hold {T} x {slots} entries")
@@ -181,7 +192,8 @@ def route_grad(dslot_w, logits, ids, S=0, renormalize=True):
     dev = logits.device
     T, E = logits.shape
     k = ids.shape[1]
-    _fit(T, E, k, S)
+    if (T | E | k | S) >> 31:
+        _too_large(T, E, k, S)
     _tensor("logits", logits, torch.float32, logits.shape)
     _tensor("ids", ids, torch.int32, (T, k), dev)
     _need(S >= 0 and dslot_w.numel() == T * (k + S), f"dslot_w must hold {T} x {k + S} entries")
@@ -197,7 +209,8 @@ def route_grad(dslot_w, logits, ids, S=0, renormalize=True):
 def _weights(w):
     """(E, N, K) of a [N][K] or [E][N][K] weight tensor."""
     _need(w.dim() in (2, 3), "w must be [N][K] or [E][N][K]")
-    _fit(*w.shape)
+    if w.numel() >> 31 and max(w.shape) >> 31:
+        _too_large(*w.shape)
     return (1, *w.shape) if w.dim() == 2 else tuple(w.shape)
 
 
@@ -230,7 +243,8 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
     dev, dt = x.device, x.dtype
     E, N, K = _weights(w)
     R = x.shape[0]
-    _fit(R, max_rows_per_expert)
+    if R >> 31 or max_rows_per_expert > 0x7FFFFFFF:
+        _too_large(R, max_rows_per_expert)
     _tensor("x", x, dt, (R, K))
     _tensor("w", w, dt, w.shape, dev)
     _offsets(offsets, E, dev)
@@ -267,7 +281,8 @@ def moe_linear_act_grad(dy, pre, activation, mul=None, offsets=None, num_experts
     dev, dt = dy.device, dy.dtype
     R, N = dy.shape
     E = num_experts if num_experts is not None else 1 if offsets is None else offsets.numel() - 1
-    _fit(R, N, E)
+    if (R | N) >> 31 or E > 0x7FFFFFFF:
+        _too_large(R, N, E)
     _tensor("dy", dy, dt, (R, N))
     _tensor("pre", pre, dt, (R, N), dev)
     if mul is not None:
@@ -294,7 +309,8 @@ def moe_linear_grad(dy, x, w, offsets=None, need_dx=True, need_dw=True, dw_dtype
     dev, dt = dy.device, dy.dtype
     E, N, K = _weights(w)
     R = dy.shape[0]
-    _fit(R)
+    if R >> 31:
+        _too_large(R)
     _tensor("dy", dy, dt, (R, N))
     _tensor("x", x, dt, (R, K), dev)
     _tensor("w", w, dt, w.shape, dev)
