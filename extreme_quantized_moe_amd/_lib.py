@@ -111,9 +111,11 @@ def lib():
         "milo_moe_w3a16_lowrank_gemm_static": (i32, [C.POINTER(MiloGemmDesc), vp]),
         "milo_moe_combine": (i32, [vp, i32, i32, i32, vp, vp]),
         "milo_moe_permute": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "milo_moe_permute_zeroed": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp]),
         "milo_moe_permute_grad": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp]),
         "milo_moe_unpermute": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
         "milo_moe_unpermute_grad": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+        "milo_moe_unpermute_grad_zeroed": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
         "milo_route_grad": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
         "milo_moe_linear_workspace_bytes": (sz, [C.POINTER(MiloLinearDesc)]),
         "milo_moe_linear": (i32, [C.POINTER(MiloLinearDesc), vp, sz, vp]),

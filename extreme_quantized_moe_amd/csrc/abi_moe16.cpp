@@ -132,14 +132,38 @@ static LinearArgs grad_args(const milo_linear_grad_desc* d, int mode) {
 
 using namespace milo;
 
+static int32_t run_permute(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
+                           int32_t num_rows, int32_t dtype, bool zero, void* y, void* stream) {
+  set_error("%s", "");
+  if (int32_t rc = check_dispatch(x, y, pair_pos, T, slots, H, num_rows, dtype)) return rc;
+  if (zero && num_rows > 0 && !y) MILO_FAIL(MILO_ERR_NULL, "the expert-ordered rows are required");
+  if (num_rows == 0 || (T == 0 && !zero)) return MILO_OK;
+  return launch_permute(x, pair_pos, T, slots, H, num_rows, dtype, zero, y, (hipStream_t)stream);
+}
+
+static int32_t run_unpermute_grad(const void* dout, const void* y, const int32_t* pair_pos, const float* slot_w,
+                                  int32_t T, int32_t slots, int32_t H, int32_t num_rows, int32_t dtype, bool zero,
+                                  void* dy, float* dslot_w, void* stream) {
+  set_error("%s", "");
+  if (int32_t rc = check_dispatch(dout, y, pair_pos, T, slots, H, num_rows, dtype)) return rc;
+  if ((T > 0 || zero) && num_rows > 0 && !dy) MILO_FAIL(MILO_ERR_NULL, "dy is required");
+  if (!aligned(slot_w, 4) || !aligned(dslot_w, 4) || !aligned(dy, elem_size(dtype)))
+    MILO_FAIL(MILO_ERR_ALIGN, "dy must be aligned to its element, slot_w and dslot_w to 4 bytes");
+  if (T == 0 && !zero) return MILO_OK;
+  return launch_unpermute_grad(dout, y, pair_pos, slot_w, T, slots, H, num_rows, dtype, zero, dy, dslot_w,
+                               (hipStream_t)stream);
+}
+
 extern "C" {
 
 int32_t milo_moe_permute(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
                          int32_t num_rows, int32_t dtype, void* y, void* stream) {
-  set_error("%s", "");
-  if (int32_t rc = check_dispatch(x, y, pair_pos, T, slots, H, num_rows, dtype)) return rc;
-  if (T == 0 || num_rows == 0) return MILO_OK;
-  return launch_permute(x, pair_pos, T, slots, H, num_rows, dtype, y, (hipStream_t)stream);
+  return run_permute(x, pair_pos, T, slots, H, num_rows, dtype, false, y, stream);
+}
+
+int32_t milo_moe_permute_zeroed(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
+                                int32_t num_rows, int32_t dtype, void* y, void* stream) {
+  return run_permute(x, pair_pos, T, slots, H, num_rows, dtype, true, y, stream);
 }
 
 int32_t milo_moe_permute_grad(const void* dy, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
@@ -159,14 +183,13 @@ int32_t milo_moe_unpermute(const void* y, const int32_t* pair_pos, const float* 
 int32_t milo_moe_unpermute_grad(const void* dout, const void* y, const int32_t* pair_pos, const float* slot_w,
                                 int32_t T, int32_t slots, int32_t H, int32_t num_rows, int32_t dtype, void* dy,
                                 float* dslot_w, void* stream) {
-  set_error("%s", "");
-  if (int32_t rc = check_dispatch(dout, y, pair_pos, T, slots, H, num_rows, dtype)) return rc;
-  if (T > 0 && num_rows > 0 && !dy) MILO_FAIL(MILO_ERR_NULL, "dy is required");
-  if (!aligned(slot_w, 4) || !aligned(dslot_w, 4) || !aligned(dy, elem_size(dtype)))
-    MILO_FAIL(MILO_ERR_ALIGN, "dy must be aligned to its element, slot_w and dslot_w to 4 bytes");
-  if (T == 0) return MILO_OK;
-  return launch_unpermute_grad(dout, y, pair_pos, slot_w, T, slots, H, num_rows, dtype, dy, dslot_w,
-                               (hipStream_t)stream);
+  return run_unpermute_grad(dout, y, pair_pos, slot_w, T, slots, H, num_rows, dtype, false, dy, dslot_w, stream);
+}
+
+int32_t milo_moe_unpermute_grad_zeroed(const void* dout, const void* y, const int32_t* pair_pos, const float* slot_w,
+                                       int32_t T, int32_t slots, int32_t H, int32_t num_rows, int32_t dtype, void* dy,
+                                       float* dslot_w, void* stream) {
+  return run_unpermute_grad(dout, y, pair_pos, slot_w, T, slots, H, num_rows, dtype, true, dy, dslot_w, stream);
 }
 
 int32_t milo_route_grad(const float* dslot_w, const float* logits, const int32_t* topk_ids, int32_t T, int32_t E,

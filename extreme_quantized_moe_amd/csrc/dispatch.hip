@@ -21,17 +21,77 @@
 
 namespace milo {
 
+// ---- rows that no pair names, as zeros (where the caller asks for it: the
+// zeros that a gradient of the experts' rows needs there).  Which they are is
+// known only from the whole table, so the first `zero_blocks` blocks of a launch
+// each scan it for a slice of the rows, mark those it names in LDS and clear the
+// others, beside the blocks that move rows: no launch and no scratch of its own.
+constexpr int kSliceRows = 1 << 15;        // at most, a multiple of 32
+
+struct Zeroing {
+  int blocks, slice;                       // blocks: 0 to leave those rows as they are
+  int64_t pairs;
+};
+
+template <class P>
+__device__ __forceinline__ void zero_free_rows(const int32_t* __restrict__ pos, const Zeroing& z, int64_t rows,
+                                               int pieces, P* __restrict__ y) {
+  struct alignas(4) Four {
+    int32_t v[4];
+  };
+  constexpr int kAhead = 8;
+  __shared__ uint32_t named[kSliceRows / 32];
+  const int64_t first = (int64_t)blockIdx.x * z.slice;
+  const int here = rows - first < z.slice ? (int)(rows - first) : z.slice;
+  for (int i = threadIdx.x; i < z.slice / 32; i += 256) named[i] = 0;
+  __syncthreads();
+  for (int64_t i = 4 * threadIdx.x; i < z.pairs; i += 1024 * kAhead) {
+    Four f[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int64_t at = i + 1024 * a;
+      if (at + 4 <= z.pairs) {
+        f[a] = *(const Four*)(pos + at);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[a].v[c] = at + c < z.pairs ? pos[at + c] : -1;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t r = (uint32_t)f[a].v[c] - (uint32_t)first;   // rows are at most 2^28: a negative entry is past `here`
+        if (r < (uint32_t)here) atomicOr(&named[r >> 5], 1u << (r & 31));
+      }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  for (int w = threadIdx.x >> 6; 32 * w < here; w += 4) {
+    uint32_t left = ~named[w];
+    if (here - 32 * w < 32) left &= (1u << (here - 32 * w)) - 1;
+    for (; left; left &= left - 1) {
+      const int64_t row = first + 32 * w + __builtin_ctz(left);
+      for (int c = lane; c < pieces; c += 64) y[row * pieces + c] = P{};
+    }
+  }
+}
+
 // ---- permute: a thread moves one V-wide piece of a token's row per step.
 // A block holds 256 / tpt tokens, tpt = threads per token (a power of two).
 // MS bounds the slots, so their positions stay in registers.
 template <class T, int V, int MS>
 __global__ void __launch_bounds__(256) permute_kernel(const typename T::store* __restrict__ x,
                                                       const int32_t* __restrict__ pos, int64_t tokens, int slots,
-                                                      int pieces, int64_t rows, int tpt_log2,
+                                                      int pieces, int64_t rows, int tpt_log2, Zeroing z,
                                                       typename T::store* __restrict__ y) {
   typedef Pack<T, V> P;
+  if (blockIdx.x < z.blocks) {
+    if (blockIdx.y == 0) zero_free_rows(pos, z, rows, pieces, (P*)y);
+    return;
+  }
   const int tpt = 1 << tpt_log2;
-  const int64_t t = (int64_t)blockIdx.x * (256 >> tpt_log2) + (threadIdx.x >> tpt_log2);
+  const int64_t t = (int64_t)(blockIdx.x - z.blocks) * (256 >> tpt_log2) + (threadIdx.x >> tpt_log2);
   if (t >= tokens) return;
   int64_t dst[MS];
 #pragma unroll
@@ -90,11 +150,15 @@ template <class T, int V, int MS, bool W, int WPT>
 __global__ void __launch_bounds__(256) unpermute_grad_kernel(
     const typename T::store* __restrict__ dout, const typename T::store* __restrict__ y,
     const int32_t* __restrict__ pos, const float* __restrict__ slot_w, int64_t tokens, int slots, int pieces,
-    int64_t rows, typename T::store* __restrict__ dy, float* __restrict__ dw) {
+    int64_t rows, Zeroing z, typename T::store* __restrict__ dy, float* __restrict__ dw) {
   typedef Pack<T, V> P;
   __shared__ float part[4][MS];
+  if (blockIdx.x < z.blocks) {
+    zero_free_rows(pos, z, rows, pieces, (P*)dy);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * (4 / WPT) + wave / WPT;
+  const int64_t t = (int64_t)(blockIdx.x - z.blocks) * (4 / WPT) + wave / WPT;
   const bool live = t < tokens;             // no early return: waves meet at a barrier
   int64_t at[MS];
   float w[MS], dot[MS];
@@ -237,13 +301,14 @@ static RowGrid row_grid(int64_t tokens, int pieces) {
   } while (0)
 
 template <class T, int V>
-static void run_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, void* y,
-                        hipStream_t st) {
+static void run_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, Zeroing z,
+                        void* y, hipStream_t st) {
   typedef typename T::store S;
   const int pieces = H / V;
-  const RowGrid g = row_grid(tokens, pieces);
+  RowGrid g = row_grid(tokens, pieces);
+  g.grid.x += z.blocks;
   MILO_SLOTS(16, hipLaunchKernelGGL((permute_kernel<T, V, MS>), g.grid, dim3(256), 0, st, (const S*)x, pos, tokens,
-                                    slots, pieces, rows, g.tpt_log2, (S*)y));
+                                    slots, pieces, rows, g.tpt_log2, z, (S*)y));
 }
 
 template <class T, int V, bool W>
@@ -258,19 +323,19 @@ static void run_unpermute(const void* y, const int32_t* pos, const float* w, int
 
 template <class T, int V, bool W>
 static void run_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
-                               int slots, int H, int64_t rows, void* dy, float* dw, hipStream_t st) {
+                               int slots, int H, int64_t rows, Zeroing z, void* dy, float* dw, hipStream_t st) {
   typedef typename T::store S;
   const int pieces = H / V;
   // four waves to a token while the tokens alone do not fill the chip (256
   // compute units x 8 waves) and the row is long enough to share
   if (tokens < 2048 && pieces > 64)
-    MILO_SLOTS(16, hipLaunchKernelGGL((unpermute_grad_kernel<T, V, MS, W, 4>), dim3((unsigned)tokens), dim3(256), 0,
-                                      st, (const S*)dout, (const S*)y, pos, w, tokens, slots, pieces, rows, (S*)dy,
-                                      dw));
-  else
-    MILO_SLOTS(16, hipLaunchKernelGGL((unpermute_grad_kernel<T, V, MS, W, 1>), dim3((unsigned)((tokens + 3) / 4)),
+    MILO_SLOTS(16, hipLaunchKernelGGL((unpermute_grad_kernel<T, V, MS, W, 4>), dim3((unsigned)tokens + z.blocks),
                                       dim3(256), 0, st, (const S*)dout, (const S*)y, pos, w, tokens, slots, pieces,
-                                      rows, (S*)dy, dw));
+                                      rows, z, (S*)dy, dw));
+  else
+    MILO_SLOTS(16, hipLaunchKernelGGL((unpermute_grad_kernel<T, V, MS, W, 1>),
+                                      dim3((unsigned)((tokens + 3) / 4) + z.blocks), dim3(256), 0, st, (const S*)dout,
+                                      (const S*)y, pos, w, tokens, slots, pieces, rows, z, (S*)dy, dw));
 }
 
 // Calls F<T, V>(args) for the type and the widest access the operands allow.
@@ -298,12 +363,47 @@ static void by_launches(int64_t tokens, Run run) {
   for (int64_t t = 0; t < tokens; t += kMostTokens) run(t, tokens - t < kMostTokens ? tokens - t : kMostTokens);
 }
 
+// ---- all rows as zeros, 4 bytes a thread and turn behind the first ones that
+// do not reach an address of 4 (2-byte types)
+__global__ void __launch_bounds__(256) zero_kernel(uint16_t* __restrict__ y, int64_t halves) {
+  const int64_t lead = ((uintptr_t)y & 2) ? 1 : 0, words = (halves - lead) / 2;
+  uint32_t* const w = (uint32_t*)(y + lead);
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (int64_t i = first; i < words; i += (int64_t)gridDim.x * 256) w[i] = 0;
+  if (first == 0 && lead) y[0] = 0;
+  if (first == 0 && (halves - lead) % 2) y[halves - 1] = 0;
+}
+
+// How the rows without a pair become zeros: by the scan where the rows' own
+// traffic hides most of it, else all rows at first, a launch and their bytes.
+// 131072 pairs to rows of 128 values of 16 bits: 8 us without, 28 with the scan,
+// 16 with the rows cleared; of 512 values 24, 32 and 37; 262144 pairs to 256
+// values 24, 55 and 43; 65536 to 2048 values 56, 61 with the scan; 8192 to 4096
+// values 16.7 and 16.5.  (512 blocks of scanning instead of 128: gradient of the 2048 values 150 us, 142 so.)
+static Zeroing plan_zeroing(bool zero, int64_t tokens, int slots, int64_t rows, int H, int dtype, void* y,
+                            hipStream_t st) {
+  if (!zero || rows == 0) return {0, 0, 0};
+  const int64_t pairs = tokens * slots, row_bytes = (int64_t)H * elem_bytes(dtype);
+  int64_t slice = (rows + 127) / 128;      // 128 blocks: few readers of the table, enough to clear many rows
+  slice = slice > kSliceRows ? kSliceRows : (slice + 31) / 32 * 32;
+  const int64_t blocks = (rows + slice - 1) / slice;
+  const double scan = 1.8e-4 * pairs * ((blocks + 127) / 128);
+  const double move = 1.8e-7 * pairs * row_bytes, clear = 4 + 1.3e-7 * rows * row_bytes;
+  if (pairs > 0 && scan < move + clear) return {(int)blocks, (int)slice, pairs};
+  const int64_t halves = rows * row_bytes / 2, want = (halves / 2 + 255) / 256;
+  hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(want < 1 ? 1 : want < 16384 ? want : 16384)), dim3(256), 0, st,
+                     (uint16_t*)y, halves);
+  return {0, 0, 0};
+}
+
 int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
-                       void* y, hipStream_t st) {
+                       bool zero, void* y, hipStream_t st) {
   const int bytes = access_bytes(H * elem_bytes(dtype), x, y);
+  const Zeroing first = plan_zeroing(zero, tokens, slots, rows, H, dtype, y, st);
 #define RUN(T, V, ...) run_permute<T, V>(__VA_ARGS__)
   by_launches(tokens, [&](int64_t t, int64_t n) {
-    MILO_BY_TYPE(RUN, (const char*)x + t * H * elem_bytes(dtype), pos + t * slots, n, slots, H, rows, y, st);
+    const Zeroing z = t == 0 ? first : Zeroing{0, 0, 0};
+    MILO_BY_TYPE(RUN, (const char*)x + t * H * elem_bytes(dtype), pos + t * slots, n, slots, H, rows, z, y, st);
   });
 #undef RUN
   return hip_status(hipGetLastError(), "permute_kernel launch");
@@ -326,14 +426,17 @@ int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int6
 }
 
 int32_t launch_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
-                              int slots, int H, int64_t rows, int dtype, void* dy, float* dw, hipStream_t st) {
+                              int slots, int H, int64_t rows, int dtype, bool zero, void* dy, float* dw,
+                              hipStream_t st) {
   const int bytes = access_bytes(H * elem_bytes(dtype), dout, y, dy);
+  const Zeroing z = plan_zeroing(zero, tokens, slots, rows, H, dtype, dy, st);
+  if (tokens == 0) return hip_status(hipGetLastError(), "zero_kernel launch");
 #define RUN(T, V, ...)                                 \
   do {                                                 \
     if (w) run_unpermute_grad<T, V, true>(__VA_ARGS__); \
     else run_unpermute_grad<T, V, false>(__VA_ARGS__);  \
   } while (0)
-  MILO_BY_TYPE(RUN, dout, y, pos, w, tokens, slots, H, rows, dy, dw, st);
+  MILO_BY_TYPE(RUN, dout, y, pos, w, tokens, slots, H, rows, z, dy, dw, st);
 #undef RUN
   return hip_status(hipGetLastError(), "unpermute_grad_kernel launch");
 }

@@ -59,11 +59,12 @@ int device_cu_count();   // compute units of the current device (abi.cpp)
 
 // rows to the experts and back (dispatch.hip)
 int32_t launch_permute(const void* x, const int32_t* pos, int64_t tokens, int slots, int H, int64_t rows, int dtype,
-                       void* y, hipStream_t st);
+                       bool zero, void* y, hipStream_t st);   // zero: rows that no pair names become zeros
 int32_t launch_unpermute(const void* y, const int32_t* pos, const float* w, int64_t tokens, int slots, int H,
                          int64_t rows, int dtype, void* out, hipStream_t st);
 int32_t launch_unpermute_grad(const void* dout, const void* y, const int32_t* pos, const float* w, int64_t tokens,
-                              int slots, int H, int64_t rows, int dtype, void* dy, float* dw, hipStream_t st);
+                              int slots, int H, int64_t rows, int dtype, bool zero, void* dy, float* dw,
+                              hipStream_t st);
 int32_t launch_route_grad(const float* dslot_w, const float* logits, const int32_t* ids, int64_t tokens, int E, int k,
                           int S, int renorm, float* dlogits, hipStream_t st);
 

@@ -93,21 +93,23 @@ def _pairs(pair_pos, slots, dev):
     return n // slots
 
 
-def _rows_out(num_rows, H, pairs, like, dropped):
-    """An expert-ordered output: zeros where rows may stay without a pair."""
+def _rows_out(name, num_rows, H, pairs, like, dropped):
+    """A new expert-ordered output, and the call that writes every row of it:
+    the _zeroed one unless the caller says that every row has a pair."""
     if num_rows >> 31:
         _too_large(num_rows)
-    new = torch.zeros if dropped or num_rows > pairs else torch.empty
-    return new((num_rows, H), dtype=like.dtype, device=like.device)
+    whole = dropped is not None and not dropped and num_rows <= pairs
+    return name if whole else name + "_zeroed", torch.empty((num_rows, H), dtype=like.dtype, device=like.device)
 
 
-def moe_permute(x, pair_pos, slots, num_rows=None, dropped=False, out=None):
+def moe_permute(x, pair_pos, slots, num_rows=None, dropped=None, out=None):
     """Rows into expert order: y[pair_pos[t, j]] = x[t].  x [T][H] fp16, bf16
     or fp32; pair_pos int32 [T*slots] as from `route_sort`, negative for a
     dropped pair.  Returns y [num_rows][H] (default T*slots).  Rows that no
-    pair names are not written: those of `out` keep their values; a new tensor
-    has zeros there when num_rows exceeds the pairs or `dropped` is set (needed
-    when pairs are dropped and rows stay free)."""
+    pair names are zeros in a new tensor; those of `out` keep their values.
+    dropped=False says that every one of at most T*slots rows has a pair, as with
+    a table straight from `route_sort`: the rows are then not looked over (up to
+    8 us for many narrow ones), and one without a pair is uninitialised."""
     code = _float_type("x", x)
     _need(x.dim() == 2, "x must be [T][H]")
     dev = x.device
@@ -118,13 +120,14 @@ def moe_permute(x, pair_pos, slots, num_rows=None, dropped=False, out=None):
     _need(_pairs(pair_pos, slots, dev) == T, f"pair_pos must hold {T} x {slots} entries")
     if out is None:
         num_rows = T * slots if num_rows is None else num_rows
-        out = _rows_out(num_rows, H, T * slots, x, dropped)
+        name, out = _rows_out("milo_moe_permute", num_rows, H, T * slots, x, dropped)
     else:
+        name = "milo_moe_permute"
         num_rows = out.shape[0] if num_rows is None else num_rows
         if num_rows >> 31:
             _too_large(num_rows)
         _tensor("out", out, x.dtype, (num_rows, H), dev)
-    _run("milo_moe_permute", dev, x.data_ptr(), pair_pos.data_ptr(), T, slots, H, num_rows, code, out.data_ptr())
+    _run(name, dev, x.data_ptr(), pair_pos.data_ptr(), T, slots, H, num_rows, code, out.data_ptr())
     return out
 
 
@@ -158,7 +161,7 @@ def moe_unpermute(y, pair_pos, slots, slot_w=None, out=None):
     return out
 
 
-def moe_unpermute_grad(dout, y, pair_pos, slots, slot_w=None, dropped=False, out=None):
+def moe_unpermute_grad(dout, y, pair_pos, slots, slot_w=None, dropped=None, out=None):
     """Gradients of `moe_unpermute`: (dy [num_rows][H], dslot_w fp32 [T*slots])
     with dy[pair_pos[t, j]] = slot_w[t, j] * dout[t] and dslot_w[t, j] =
     <dout[t], y[pair_pos[t, j]]>.  Rows of dy without a pair: as in
@@ -176,12 +179,13 @@ def moe_unpermute_grad(dout, y, pair_pos, slots, slot_w=None, dropped=False, out
     if slot_w is not None:
         _tensor("slot_w", slot_w, torch.float32, pair_pos.shape, dev)
     if out is None:
-        out = _rows_out(R, H, T * slots, dout, dropped)
+        name, out = _rows_out("milo_moe_unpermute_grad", R, H, T * slots, dout, dropped)
     else:
+        name = "milo_moe_unpermute_grad"
         _tensor("out", out, dout.dtype, (R, H), dev)
     dw = torch.empty(pair_pos.shape, dtype=torch.float32, device=dev)
-    _run("milo_moe_unpermute_grad", dev, dout.data_ptr(), y.data_ptr(), pair_pos.data_ptr(), _ptr(slot_w), T, slots,
-         H, R, code, out.data_ptr(), dw.data_ptr())
+    _run(name, dev, dout.data_ptr(), y.data_ptr(), pair_pos.data_ptr(), _ptr(slot_w), T, slots, H, R, code,
+         out.data_ptr(), dw.data_ptr())
     return out, dw
 
 
@@ -350,7 +354,7 @@ class MoELayer16:
         _tensor("logits", logits, torch.float32, (T, self.E), self.w1.device)
         r = route_sort(logits, self.k, self.S, self.renormalize, own_scratch=True)
         off = r["offsets"]
-        xs = moe_permute(x, r["pair_pos"], slots)
+        xs = moe_permute(x, r["pair_pos"], slots, dropped=False)
         up = moe_linear(xs, self.w3, off, max_rows_per_expert=T)
         got = moe_linear(xs, self.w1, off, activation="silu", mul=up, return_pre=keep, max_rows_per_expert=T)
         h, pre = got if keep else (got, None)
@@ -362,7 +366,7 @@ class MoELayer16:
         """Gradients of x, the logits and the three weights for dout [T][H]."""
         r, slots = kept["route"], self.k + self.S
         off = r["offsets"]
-        dy, dslot = moe_unpermute_grad(dout, kept["y"], r["pair_pos"], slots, r["slot_w"])
+        dy, dslot = moe_unpermute_grad(dout, kept["y"], r["pair_pos"], slots, r["slot_w"], dropped=False)
         dlogits = route_grad(dslot, kept["logits"], r["ids"], self.S, self.renormalize)
         dh, dw2 = moe_linear_grad(dy, kept["h"], self.w2, off, dw_dtype=dw_dtype)
         dpre, dup, _ = moe_linear_act_grad(dh, kept["pre"], "silu", mul=kept["up"], offsets=off)

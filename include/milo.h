@@ -527,7 +527,9 @@ enum { MILO_F16 = 0, MILO_BF16 = 1, MILO_F32 = 2 };
  *                   dslot_w[t,j] = <dout[t], y[pair_pos[t,j]]> (0 if dropped)
  * Sums run in float32, in slot order (dslot_w: in a fixed order over the
  * row), and are rounded once.  A token without a kept pair gets zeros.  Rows
- * of an expert-ordered output that no pair names are not written.
+ * of an expert-ordered output that no pair names are not written, by the
+ * _zeroed forms as zeros (the whole buffer, also with T == 0): a buffer that was
+ * never written must not reach the experts' gradients.
  *
  * x, out, dout, dx : [T][H];  y, dy : [num_rows][H], all of type dtype
  *   (MILO_F16, MILO_BF16 or MILO_F32).  Outputs must not overlap inputs.
@@ -540,6 +542,8 @@ enum { MILO_F16 = 0, MILO_BF16 = 1, MILO_F32 = 2 };
  */
 int32_t milo_moe_permute(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
                          int32_t num_rows, int32_t dtype, void* y, void* stream);
+int32_t milo_moe_permute_zeroed(const void* x, const int32_t* pair_pos, int32_t T, int32_t slots,
+                                int32_t H, int32_t num_rows, int32_t dtype, void* y, void* stream);
 int32_t milo_moe_permute_grad(const void* dy, const int32_t* pair_pos, int32_t T, int32_t slots, int32_t H,
                               int32_t num_rows, int32_t dtype, void* dx, void* stream);
 int32_t milo_moe_unpermute(const void* y, const int32_t* pair_pos, const float* slot_w, int32_t T,
@@ -548,6 +552,10 @@ int32_t milo_moe_unpermute(const void* y, const int32_t* pair_pos, const float* 
 int32_t milo_moe_unpermute_grad(const void* dout, const void* y, const int32_t* pair_pos,
                                 const float* slot_w, int32_t T, int32_t slots, int32_t H,
                                 int32_t num_rows, int32_t dtype, void* dy, float* dslot_w, void* stream);
+int32_t milo_moe_unpermute_grad_zeroed(const void* dout, const void* y, const int32_t* pair_pos,
+                                       const float* slot_w, int32_t T, int32_t slots, int32_t H,
+                                       int32_t num_rows, int32_t dtype, void* dy, float* dslot_w,
+                                       void* stream);
 
 /*
  * Gradient of milo_route_sort's routed weights with respect to the logits
