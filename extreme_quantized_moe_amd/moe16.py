@@ -34,6 +34,19 @@ def _tensor(name, t, dtype, shape, dev=None):
     raise ValueError(f"{name} is on {t.device}, the first operand on {dev}")
 
 
+def _apart(out, *inputs, same=()):
+    """Refuses an `out` that shares memory with an input: other threads would
+    read what was just written.  same: inputs that may be `out` itself."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for i, t in enumerate((*inputs, *same)):
+        if t is None:
+            continue
+        a, n = t.data_ptr(), t.numel() * t.element_size()
+        if a < hi and lo < a + n and (i < len(inputs) or a != lo or t.dtype != out.dtype):
+            raise ValueError("out shares memory with an input")
+
+
 def _float_type(name, t, wide=True):
     code = _DTYPES.get(t.dtype)
     if code is None or (code == L.F32 and not wide):
@@ -127,6 +140,7 @@ def moe_permute(x, pair_pos, slots, num_rows=None, dropped=None, out=None):
         if num_rows >> 31:
             _too_large(num_rows)
         _tensor("out", out, x.dtype, (num_rows, H), dev)
+        _apart(out, x, pair_pos)
     _run(name, dev, x.data_ptr(), pair_pos.data_ptr(), T, slots, H, num_rows, code, out.data_ptr())
     return out
 
@@ -156,6 +170,7 @@ def moe_unpermute(y, pair_pos, slots, slot_w=None, out=None):
         out = torch.empty((T, H), dtype=y.dtype, device=dev)
     else:
         _tensor("out", out, y.dtype, (T, H), dev)
+        _apart(out, y, pair_pos, slot_w)
     _run("milo_moe_unpermute", dev, y.data_ptr(), pair_pos.data_ptr(), _ptr(slot_w), T, slots, H, R, code,
          out.data_ptr())
     return out
@@ -183,6 +198,7 @@ def moe_unpermute_grad(dout, y, pair_pos, slots, slot_w=None, dropped=None, out=
     else:
         name = "milo_moe_unpermute_grad"
         _tensor("out", out, dout.dtype, (R, H), dev)
+        _apart(out, dout, y, pair_pos, slot_w)
     dw = torch.empty(pair_pos.shape, dtype=torch.float32, device=dev)
     _run(name, dev, dout.data_ptr(), y.data_ptr(), pair_pos.data_ptr(), _ptr(slot_w), T, slots, H, R, code,
          out.data_ptr(), dw.data_ptr())
@@ -240,7 +256,9 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
     residual [rows][N]; activation "none", "relu", "silu", "gelu" or
     "gelu_tanh".  Returns y [rows][N] in x's type or out_dtype float32, and
     with return_pre also the pre-activation in x's type.  Rows outside the
-    offsets are not written (a new tensor is uninitialised there).
+    offsets are not written (a new tensor is uninitialised there).  out: may be
+    mul or residual itself where the types are equal, and shares no memory with
+    another operand.
     max_rows_per_expert: a bound the caller knows, for the kernel choice."""
     code = _float_type("x", x, wide=False)
     _need(x.dim() == 2, "x must be [rows][K]")
@@ -264,6 +282,7 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
         out = torch.empty((R, N), dtype=odt, device=dev)
     else:
         _tensor("out", out, odt, (R, N), dev)
+        _apart(out, x, w, offsets, bias, same=(mul, residual))
     pre = torch.empty((R, N), dtype=dt, device=dev) if return_pre else None
     ref = C.byref(L.MiloLinearDesc(
         E, N, K, R, max_rows_per_expert, code, L.F32 if odt is torch.float32 else code, _act(activation), x.data_ptr(),
