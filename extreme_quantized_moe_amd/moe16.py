@@ -367,11 +367,11 @@ class MoELayer16:
 
     def forward(self, x, logits, keep=False):
         """x [T][H] and float32 logits [T][E] to out [T][H]; with keep also what
-        `backward` takes."""
+        `backward` takes.  At most 65536 tokens (`route_sort`'s bound), or none."""
         T, slots = x.shape[0], self.k + self.S
         logits = logits.contiguous()
         _tensor("logits", logits, torch.float32, (T, self.E), self.w1.device)
-        r = route_sort(logits, self.k, self.S, self.renormalize, own_scratch=True)
+        r = route_sort(logits, self.k, self.S, self.renormalize, own_scratch=True) if T else self._no_route(logits)
         off = r["offsets"]
         xs = moe_permute(x, r["pair_pos"], slots, dropped=False)
         up = moe_linear(xs, self.w3, off, max_rows_per_expert=T)
@@ -380,6 +380,14 @@ class MoELayer16:
         y = moe_linear(h, self.w2, off, max_rows_per_expert=T)
         out = moe_unpermute(y, r["pair_pos"], slots, r["slot_w"])
         return (out, dict(route=r, logits=logits, xs=xs, up=up, pre=pre, h=h, y=y)) if keep else out
+
+    def _no_route(self, logits):
+        """What `route_sort` gives, for no token (it takes one at least)."""
+        def of(dt, *shape):
+            return torch.zeros(shape, dtype=dt, device=logits.device)
+        i32, f32 = torch.int32, torch.float32
+        return dict(ids=of(i32, 0, self.k), w=of(f32, 0, self.k), slot_w=of(f32, 0), sorted_pairs=of(i32, 0),
+                    pair_pos=of(i32, 0), offsets=of(i32, self.E + self.S + 1))
 
     def backward(self, dout, kept, dw_dtype=None):
         """Gradients of x, the logits and the three weights for dout [T][H]."""
