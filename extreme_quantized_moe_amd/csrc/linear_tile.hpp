@@ -317,6 +317,16 @@ __device__ __forceinline__ u32x4 rounded(const float* v) {
   return __builtin_bit_cast(u32x4, o);
 }
 
+// Orders a wave's LDS accesses where its lanes read what others of them wrote:
+// the hardware runs a wave's LDS instructions in order, this keeps the compiler
+// from moving them past each other.  No instruction.
+__device__ __forceinline__ void wave_in_order() {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#endif
+}
+
 // Results of a wave for arrays of any alignment and row length: 64 rows x 64
 // columns from row m, column n on, turned around in the wave's own LDS (16-byte
 // piece c of row r at place c ^ (r mod 16)), so that a lane gets 8 consecutive
@@ -326,11 +336,13 @@ template <class T, int MODE>
 __device__ __forceinline__ void finish_turned(const LinearArgs& a, int e, int base, int M, int m0, int n0, int split,
                                               char* mine, const f32x4 (*acc)[4]) {
   const int lane = threadIdx.x & 63, r0 = lane & 15, cols = MODE == kFwd ? a.N : a.K;
+  wave_in_order();                         // the rows before have been read
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *(f32x4*)(mine + (16 * i + r0) * 256 + (((4 * j + (lane >> 4)) ^ r0) << 4)) = acc[i][j];
+  wave_in_order();                         // all lanes' results are there
   LinearArgs to = a;
   if (a.splits > 1) {                      // this split's sums as they are
     to.out = a.part + (int64_t)split * (MODE == kDw ? (int64_t)a.E * a.N : a.rows) * cols;
