@@ -120,10 +120,16 @@ __device__ __forceinline__ TileSlot find_slot(const int32_t* __restrict__ offset
 // Float32 values, a few instructions each: in the tile kernel's epilogue and in
 // the activation gradient they run once per output on the vector units, 16
 // lanes a cycle, with nothing else to hide behind.  Tails are computed without
-// cancellation (sigmoid from exp(-|v|), the normal distribution from erfcx), so
-// they hold float32 relative precision down to results of 2^-126, which the
-// exponential flushes to zero.  Arguments are bounded where a product of 0 and
-// infinity would appear.  NaN stays NaN.
+// cancellation (sigmoid from exp(-|v|), the normal distribution from erfcx), down
+// to results of 2^-126, which the exponential flushes to zero.  The exponential
+// takes a rounded argument, so a tail's relative error grows with the argument a:
+// at most 1.25 a + 10 roundings of 2^-24 for SILU (a = |v|), 1.25 a + 22 for GELU
+// (a = v^2 / 2), 6.5 a + 12 for GELU_TANH, whose argument a = 2 sqrt(2/pi) |v +
+// 0.044715 v^3| is itself computed.  With a < 88 that stays under a tenth of a
+// 16-bit rounding (2^-15 against 2^-12 for fp16); float32 results show it, and a
+// second word of the argument would cost the epilogue four more instructions a
+// value.  Arguments are bounded where a product of 0 and infinity would appear.
+// NaN stays NaN.
 __device__ __forceinline__ float bounded(float v, float lo, float hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 constexpr float kLog2e = 1.4426950408889634f;
