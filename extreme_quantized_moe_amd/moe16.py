@@ -397,6 +397,10 @@ class MoELayer16:
         dlogits = route_grad(dslot, kept["logits"], r["ids"], self.S, self.renormalize)
         dh, dw2 = moe_linear_grad(dy, kept["h"], self.w2, off, dw_dtype=dw_dtype)
         dpre, dup, _ = moe_linear_act_grad(dh, kept["pre"], "silu", mul=kept["up"], offsets=off)
+        # xs feeds two products: the up product's half of its gradient is rounded to
+        # 16 bits, the gate's is added to it in float32.  One more half step of the
+        # type that the sum is rounded to next; a float32 half would be 4 bytes more
+        # to write and to read for every value.
         dxs, dw3 = moe_linear_grad(dup, kept["xs"], self.w3, off, dw_dtype=dw_dtype)
         dxs, dw1 = moe_linear_grad(dpre, kept["xs"], self.w1, off, dw_dtype=dw_dtype, dx_add=dxs)
         return dict(dx=moe_permute_grad(dxs, r["pair_pos"], slots), dlogits=dlogits, dw1=dw1, dw3=dw3, dw2=dw2)
