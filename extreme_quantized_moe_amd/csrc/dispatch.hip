@@ -14,9 +14,13 @@
 // Sums run in float32 in a fixed order (slots, then lanes, then waves) and
 // are rounded once.  A position at or past `rows` counts as dropped, so no
 // table makes a kernel touch memory outside the buffers.  Measured (MI355X, a
-// large copy runs at 4.7 TB/s): 4096 rows of 4096 bf16 values to two slots each
-// 16 us and back 17 (5.9 TB/s: part of it stays in the last-level cache); 8192
-// rows of 2048 over eight slots, both gradients 130 us (4.5 TB/s) and 67 (4.5).
+// large copy runs at 4.7 to 4.9 TB/s): 4096 rows of 4096 bf16 values to two slots
+// each 17 us and back 18 (5.9 TB/s: part of it stays in the last-level cache);
+// 8192 rows of 2048 over eight slots, gradient of the way back 128 us (4.5 TB/s),
+// of the way there 67 with pairs spread at random (4.5) and 86 with the few
+// destinations of skewed experts (3.5: its blocks live for one token, with two
+// dependent loads and a store).  Rows of 2047 values go by 2 bytes an access: there
+// 132 us (2048: 61), back 69 (80), gradients 217 (143) and 66 (69).
 #include "half_types.hpp"
 
 namespace milo {

@@ -3,7 +3,9 @@
 //   dpre = dy mul act'(pre),  dmul = dy act(pre),
 //   dbias[e] = sum of dpre (before its rounding) over expert e's rows.
 // Bound by HBM (dy, pre and mul read once, dpre and dmul written once): 8192 x
-// 14336 bf16 with gate operand 210 us, 5.6 TB/s.
+// 14336 bf16 with gate operand 210 to 222 us, 5.3 to 5.6 TB/s; with bias gradients
+// of one expert 221, and 28 for the sum of its 256 row groups.  8192 x 14335 goes by
+// 2 bytes an access: 257 and 350.
 #include "linear.hpp"
 
 namespace milo {

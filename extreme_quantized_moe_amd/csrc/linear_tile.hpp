@@ -8,9 +8,9 @@
 // 64 KB buffers): of the wave shapes that fit, the one whose LDS reads (192 KB
 // a step at 128 bytes a cycle) stay under its products (2048 cycles); four
 // waves of 128 x 128 would read a third less but the compiler then copies
-// accumulators around.  8192 x 14336 x 4096 bf16: forward 690 us, dx 700, dw
-// 775 (1390, 1370, 1240 TFLOP/s; the library's product on the same card 1330,
-// with the transposed operand 1310).  128 x 128 tiles, four waves of 64 x 64,
+// accumulators around.  8192 x 14336 x 4096 bf16: forward 710 us, dx 752, dw
+// 780 (1355, 1280, 1235 TFLOP/s; the library's products timed in turn on the same
+// card 612, 693 and 956 us).  128 x 128 tiles, four waves of 64 x 64,
 // two blocks a compute unit, where 256 x 256 tiles would not fill the chip.
 //
 // Operands go from memory straight into LDS, 16 bytes a lane, through buffer

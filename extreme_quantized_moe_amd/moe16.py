@@ -2,7 +2,9 @@
 the experts and back, grouped products with an epilogue, their gradients, and
 `MoELayer16`, the unquantized counterpart of `MoELayer` with a backward pass.
 Calls run on the tensors' device, on its current stream, and allocate their
-outputs and scratch from torch's allocator; nothing is kept between calls."""
+outputs and scratch from torch's allocator; nothing is kept between calls.
+They stand outside autograd: results carry no graph, also of operands that
+require gradients, and the gradients are calls of their own."""
 import ctypes as C
 
 import torch
@@ -259,7 +261,9 @@ def moe_linear(x, w, offsets=None, bias=None, activation="none", mul=None, resid
     offsets are not written (a new tensor is uninitialised there).  out: may be
     mul or residual itself where the types are equal, and shares no memory with
     another operand.
-    max_rows_per_expert: a bound the caller knows, for the kernel choice."""
+    max_rows_per_expert: a bound the caller knows, for the kernel choice.
+    Scratch: with K no multiple of 8 (or w off a 16-byte address) and many rows
+    it holds a copy of w in whole rows, made in every call."""
     code = _float_type("x", x, wide=False)
     _need(x.dim() == 2, "x must be [rows][K]")
     dev, dt = x.device, x.dtype

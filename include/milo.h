@@ -600,7 +600,11 @@ int32_t milo_route_grad(const float* dslot_w, const float* logits, const int32_t
  *             correctness.
  * workspace : milo_moe_linear_workspace_bytes(desc) bytes (may be 0), 256-byte
  *             aligned, scratch only; the size is that of this desc, its
- *             pointers' alignment included.  Calls that overlap in time need
+ *             pointers' alignment included.  It holds partial sums where the
+ *             contraction is split and, where an operand's rows do not start on
+ *             16-byte addresses and the rows are many, a copy of that operand
+ *             made in every call: of all weights (num_experts N K elements, K
+ *             rounded up) where K is no multiple of 8.  Calls that overlap in time need
  *             workspaces of their own.
  * Capturable into a HIP graph.  Constraints: 1 <= num_experts <= 256,
  * 1 <= N, K <= 65536, 0 <= num_rows <= 2^20, all pointers aligned to their element (16 bytes, with N
