@@ -27,7 +27,7 @@ namespace milo {
 
 // ---- rows that no pair names, as zeros (where the caller asks for it: the
 // zeros that a gradient of the experts' rows needs there).  Which they are is
-// known only from the whole table, so the first `zero_blocks` blocks of a launch
+// known only from the whole table, so the first blocks of a launch (Zeroing)
 // each scan it for a slice of the rows, mark those it names in LDS and clear the
 // others, beside the blocks that move rows: no launch and no scratch of its own.
 constexpr int kSliceRows = 1 << 15;        // at most, a multiple of 32
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(256) zero_kernel(uint16_t* __restrict__ y, int
 // 131072 pairs to rows of 128 values of 16 bits: 8 us without, 28 with the scan,
 // 16 with the rows cleared; of 512 values 24, 32 and 37; 262144 pairs to 256
 // values 24, 55 and 43; 65536 to 2048 values 56, 61 with the scan; 8192 to 4096
-// values 16.7 and 16.5.  (512 blocks of scanning instead of 128: gradient of the 2048 values 150 us, 142 so.)
+// values 16.7 and 16.5.  (With 512 blocks of scanning instead of 128 the gradient
+// of the 2048 values took 150 us, 142 so.)
 static Zeroing plan_zeroing(bool zero, int64_t tokens, int slots, int64_t rows, int H, int dtype, void* y,
                             hipStream_t st) {
   if (!zero || rows == 0) return {0, 0, 0};

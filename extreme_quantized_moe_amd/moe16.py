@@ -123,8 +123,9 @@ def moe_permute(x, pair_pos, slots, num_rows=None, dropped=None, out=None):
     dropped pair.  Returns y [num_rows][H] (default T*slots).  Rows that no
     pair names are zeros in a new tensor; those of `out` keep their values.
     dropped=False says that every one of at most T*slots rows has a pair, as with
-    a table straight from `route_sort`: the rows are then not looked over (up to
-    8 us for many narrow ones), and one without a pair is uninitialised."""
+    a table straight from `route_sort`: the rows are then not looked over (which
+    takes some microseconds for many narrow ones), and one without a pair is
+    uninitialised."""
     code = _float_type("x", x)
     _need(x.dim() == 2, "x must be [T][H]")
     dev = x.device
